@@ -1,5 +1,6 @@
-"""Python binding of the routed MoE layer's C ABI (``include/moe.h``, and the
-roofline measurement kernels of ``include/moe_peak.h``).
+"""Python binding of the routed MoE layer's C ABI (``include/moe.h``, the FP8
+operators of ``include/moe_fp8.h``, and the roofline measurement kernels of
+``include/moe_peak.h``).
 
 Argument marshalling only: every step of the layer runs in the HIP kernels of
 ``libqrmoe.so``.  torch supplies device memory (tensors) and the stream
@@ -14,6 +15,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from contextlib import nullcontext
 from dataclasses import dataclass
 from typing import Optional
 
@@ -46,6 +48,9 @@ MOE_LAYOUT_TILES = 1
 
 MOE_SLOT_SKIP = -2
 
+MOE_TYPE_BF16 = 1
+MOE_TYPE_F32 = 2
+
 # Every symbol include/moe.h declares.
 EXPORTS = (
     "moe_workspace_bytes", "moe_workspace_init", "moe_route_topk", "moe_dispatch",
@@ -56,6 +61,9 @@ EXPORTS = (
     "moe_workspace_bytes_mx8", "moe_expert_ffn_mx8", "moe_layer_mx8_workspace_bytes", "moe_layer_mx8",
     "moe_workspace_bytes_mx4", "moe_expert_ffn_mx4", "moe_layer_mx4_workspace_bytes", "moe_layer_mx4",
     "moe_slab_layout", "moe_bank_slots", "moe_layer_noalloc",
+    # include/moe_fp8.h
+    "moe_add_rmsnorm", "moe_gemm_fp8", "moe_grouped_gemm_fp8", "moe_expert_gate_up_fp8_workspace_bytes",
+    "moe_expert_gate_up_fp8", "moe_layer_fp8_workspace_bytes", "moe_layer_fp8",
     # include/moe_peak.h
     "moe_peak_stream", "moe_peak_mfma", "moe_peak_hold",
 )
@@ -83,6 +91,10 @@ class moe_experts(ctypes.Structure):
                 ("slot_bytes", ctypes.c_uint64)]
 
 
+class moe_fp8_experts(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("gate", "gate_scales", "up", "up_scales", "down", "down_scales")]
+
+
 class moe_bank(ctypes.Structure):
     _fields_ = [("E", ctypes.c_int32), ("num_slots", ctypes.c_int32), ("slot_of_expert", ctypes.c_void_p),
                 ("expert_of_slot", ctypes.c_void_p), ("last_use", ctypes.c_void_p), ("clock", ctypes.c_uint64),
@@ -98,6 +110,7 @@ _LIB = None
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _SZ = ctypes.c_size_t
+_I64 = ctypes.c_int64
 
 
 def lib() -> ctypes.CDLL:
@@ -143,6 +156,13 @@ def lib() -> ctypes.CDLL:
             "moe_slab_layout": (_SZ, [_I, _I, _I, _P]),
             "moe_bank_slots": (_I, [_I, _P, ctypes.c_uint64, ctypes.c_uint64, ctypes.c_uint64, _P]),
             "moe_layer_noalloc": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P]),
+            "moe_add_rmsnorm": (_I, [_I, _I, _P, _I, _I64, _P, _P, _I, _I64, _I64, _P, _I, ctypes.c_float, _P, _P, _P, _P]),
+            "moe_gemm_fp8": (_I, [_I, _I, _I, _P, _I64, _P, _P, _P, _P, _I, _I64, _P]),
+            "moe_grouped_gemm_fp8": (_I, [_I, _I, _I, _I, _P, _I, _P, _P, _P, _P, _P, _I, _P, _I, _P]),
+            "moe_expert_gate_up_fp8_workspace_bytes": (_SZ, [_P]),
+            "moe_expert_gate_up_fp8": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+            "moe_layer_fp8_workspace_bytes": (_SZ, [_P]),
+            "moe_layer_fp8": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
             "moe_peak_stream": (_I, [_P, _SZ, ctypes.c_int32, _P, _P]),
             "moe_peak_mfma": (_I, [ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, _P, _P]),
             "moe_peak_hold": (_I, [ctypes.c_uint32, _P]),
@@ -617,6 +637,269 @@ def layer_shared(x, experts: Experts, shared: Experts, k: int, *, w_router=None,
     _check(rc, "moe_layer_shared")
     if check:
         check_device_status(ws, "layer_shared", stream)
+    return out, ids, w, logits
+
+
+# -------------------------------------------------------------- FP8 operators
+
+def _codes(t, shape, name):
+    """Address of E4M3 codes (float8_e4m3fn or uint8) of the given shape."""
+    torch = _torch()
+    p = _ptr(t, (torch.float8_e4m3fn, torch.uint8), name)
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    return p
+
+
+def _sized(t, shape, dtype, name):
+    p = _ptr(t, dtype, name)
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    return p
+
+
+def _runs(n: int) -> int:
+    """Runs of 128 in n values."""
+    return (n + 127) // 128
+
+
+def _moe_type(dtype, name: str) -> int:
+    torch = _torch()
+    if dtype == torch.bfloat16:
+        return MOE_TYPE_BF16
+    if dtype == torch.float32:
+        return MOE_TYPE_F32
+    raise ValueError(f"{name} has dtype {dtype}, expected torch.bfloat16 or torch.float32")
+
+
+def _rows(t, name: str):
+    """(address, stride in values) of a 2-D device tensor whose rows are
+    contiguous (they may lie apart)."""
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}'s rows must be contiguous")
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def _scope(name: str, stream, first, *others):
+    """The scope of a call on the device of `first`, on `stream` (default: the
+    current stream of that device): inside it the device and the stream are
+    the current ones, so that what the call allocates belongs to the stream
+    that uses it."""
+    torch = _torch()
+    dev = first.device
+    if dev.type != "cuda":
+        raise ValueError(f"{name} takes device tensors")
+    for t in others:
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name}: tensors on {dev} and {t.device}")
+    if stream is not None:
+        if stream.device != dev:
+            raise ValueError(f"{name}: tensors on {dev}, stream of {stream.device}")
+        return torch.cuda.stream(stream)
+    return nullcontext() if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+
+
+def _call(name: str, *args) -> None:
+    _check(getattr(lib(), name)(*args, _torch().cuda.current_stream().cuda_stream), name)
+
+
+def add_rmsnorm(x, weight=None, *, residual=None, residual_out=None, eps: float = 1e-6, y: bool = True,
+                fp8: bool = False, stream=None):
+    """moe_add_rmsnorm on rows x [T][d] (bf16 or fp32): h = x + residual,
+    kept in the residual's type; the norm of h times `weight` as bf16 (`y`)
+    and as E4M3 codes with a scale per run of 128 (`fp8`).  `residual_out`
+    takes h (it may be `residual`: in place); by default a new tensor.
+    Returns (y, residual_out, q, q_scales), None for what was not asked."""
+    torch = _torch()
+    xp, xs = _rows(x, "x")
+    T, d = x.shape
+    xt = _moe_type(x.dtype, "x")
+    if residual is not None:
+        if residual.shape != x.shape:
+            raise ValueError(f"residual has shape {tuple(residual.shape)}, x {tuple(x.shape)}")
+        if residual_out is not None and (residual_out.shape != x.shape or residual_out.dtype != residual.dtype):
+            raise ValueError("residual_out must have the residual's shape and dtype")
+    elif residual_out is not None:
+        raise ValueError("residual_out without residual")
+    wp = None if weight is None else _sized(weight, (d,), weight.dtype, "weight")
+    wt = 0 if weight is None else _moe_type(weight.dtype, "weight")
+    with _scope("add_rmsnorm", stream, x, residual, residual_out, weight):
+        dev = x.device
+        rp = rop = None
+        rt = rs = ros = 0
+        if residual is not None:
+            rp, rs = _rows(residual, "residual")
+            rt = _moe_type(residual.dtype, "residual")
+            if residual_out is None:
+                residual_out = torch.empty((T, d), dtype=residual.dtype, device=dev)
+            rop, ros = _rows(residual_out, "residual_out")
+        yt = torch.empty((T, d), dtype=torch.bfloat16, device=dev) if y else None
+        q = torch.empty((T, d), dtype=torch.float8_e4m3fn, device=dev) if fp8 else None
+        sc = torch.empty((T, _runs(d)), dtype=torch.float32, device=dev) if fp8 else None
+        _call("moe_add_rmsnorm", T, d, xp, xt, xs, rp, rop, rt, rs, ros, wp, wt, eps, yt.data_ptr() if y else None,
+              q.data_ptr() if fp8 else None, sc.data_ptr() if fp8 else None)
+    return yt, residual_out, q, sc
+
+
+def gemm_fp8(a, a_scales, w, w_scales, *, out=None, out_dtype=None, stream=None):
+    """moe_gemm_fp8: out [M][N] = a [M][K] . w [N][K]^T, E4M3 codes with one
+    fp32 scale per run of 128 of a's rows (a_scales [M][ceil(K/128)]) and per
+    128 x 128 block of w (w_scales [ceil(N/128)][ceil(K/128)]).  a's and
+    out's rows may lie apart.  out_dtype: torch.bfloat16 (default) or
+    torch.float32; `out` brings its own."""
+    torch = _torch()
+    if a.dtype not in (torch.float8_e4m3fn, torch.uint8):
+        raise ValueError(f"a has dtype {a.dtype}, expected torch.float8_e4m3fn or torch.uint8")
+    ap, lda = _rows(a, "a")
+    M, K = a.shape
+    N = w.shape[0]
+    if out is not None and (tuple(out.shape) != (M, N) or (out_dtype is not None and out.dtype != out_dtype)):
+        raise ValueError(f"out must be {out_dtype or out.dtype} of shape {(M, N)}")
+    asp = _sized(a_scales, (M, _runs(K)), torch.float32, "a_scales")
+    wp = _codes(w, (N, K), "w")
+    wsp = _sized(w_scales, (_runs(N), _runs(K)), torch.float32, "w_scales")
+    with _scope("gemm_fp8", stream, a, a_scales, w, w_scales, out):
+        if out is None:
+            out = torch.empty((M, N), dtype=out_dtype or torch.bfloat16, device=a.device)
+        op, ldo = _rows(out, "out")
+        _call("moe_gemm_fp8", M, N, K, ap, lda, asp, wp, wsp, op, _moe_type(out.dtype, "out"), ldo)
+    return out
+
+
+def grouped_gemm_fp8(a, a_scales, w, w_scales, offsets, *, perm=None, k: int = 1, out=None, out_dtype=None,
+                     stream=None):
+    """moe_grouped_gemm_fp8: sorted rows offsets[e] .. offsets[e+1] times
+    w[e] ([E][N][K]); row r reads a[r], or a[perm[r] // k] with `perm` (int32,
+    one entry per sorted row).  Returns out [rows][N], torch.float32 by
+    default (what moe_combine takes)."""
+    torch = _torch()
+    a_rows, K = a.shape
+    E, N = w.shape[:2]
+    R = a_rows if perm is None else perm.numel()
+    ap = _codes(a, (a_rows, K), "a")
+    asp = _sized(a_scales, (a_rows, _runs(K)), torch.float32, "a_scales")
+    wp = _codes(w, (E, N, K), "w")
+    wsp = _sized(w_scales, (E, _runs(N), _runs(K)), torch.float32, "w_scales")
+    offp = _sized(offsets, (E + 1,), torch.int32, "offsets")
+    permp = None if perm is None else _sized(perm, (R,), torch.int32, "perm")
+    if out is not None and out_dtype is not None and out.dtype != out_dtype:
+        raise ValueError(f"out must be {out_dtype}")
+    with _scope("grouped_gemm_fp8", stream, a, a_scales, w, w_scales, offsets, perm, out):
+        if out is None:
+            out = torch.empty((R, N), dtype=out_dtype or torch.float32, device=a.device)
+        if R:
+            _call("moe_grouped_gemm_fp8", R, E, N, K, ap, a_rows, asp, wp, wsp, offp, permp, int(k),
+                  _sized(out, (R, N), out.dtype, "out"), _moe_type(out.dtype, "out"))
+    return out
+
+
+def expert_gate_up_fp8(a, a_scales, gate, gate_scales, up, up_scales, offsets, perm, k: int, *, act=None,
+                       act_scales=None, ws=None, stream=None):
+    """moe_expert_gate_up_fp8: silu(gate[e] a) * (up[e] a) of every sorted row
+    (token perm[r] // k of a [T][d]; gate, up [E][f][d]) as E4M3 codes with a
+    scale per run of 128.  Returns (act [T*k][f], act_scales), the `a` of a
+    grouped_gemm_fp8 with the down matrices.  ws: a uint8 tensor of
+    moe_expert_gate_up_fp8_workspace_bytes, allocated by default."""
+    torch = _torch()
+    T, d = a.shape
+    E, f = gate.shape[:2]
+    R = T * k
+    shape = moe_shape(T, d, E, k, f)
+    ptrs = (_codes(a, (T, d), "a"), _sized(a_scales, (T, _runs(d)), torch.float32, "a_scales"),
+            _codes(gate, (E, f, d), "gate"), _sized(gate_scales, (E, _runs(f), _runs(d)), torch.float32, "gate_scales"),
+            _codes(up, (E, f, d), "up"), _sized(up_scales, (E, _runs(f), _runs(d)), torch.float32, "up_scales"),
+            _sized(offsets, (E + 1,), torch.int32, "offsets"), _sized(perm, (R,), torch.int32, "perm"))
+    with _scope("expert_gate_up_fp8", stream, a, a_scales, gate, gate_scales, up, up_scales, offsets, perm, act,
+                act_scales, ws):
+        dev = a.device
+        if act is None:
+            act = torch.empty((R, f), dtype=torch.float8_e4m3fn, device=dev)
+        if act_scales is None:
+            act_scales = torch.empty((R, _runs(f)), dtype=torch.float32, device=dev)
+        if ws is None:
+            n = int(lib().moe_expert_gate_up_fp8_workspace_bytes(ctypes.byref(shape)))
+            ws = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
+        _call("moe_expert_gate_up_fp8", ctypes.byref(shape), *ptrs, _codes(act, (R, f), "act"),
+              _sized(act_scales, (R, _runs(f)), torch.float32, "act_scales"), _ptr(ws, name="ws", allow_none=True),
+              0 if ws is None else ws.numel() * ws.element_size())
+    return act, act_scales
+
+
+@dataclass
+class ExpertsFp8:
+    """The experts of one FP8 layer: E4M3 codes (float8_e4m3fn or uint8) and
+    fp32 scales per 128 x 128 block; gate and up [E][f][d], down [E][d][f]."""
+    gate: object
+    gate_scales: object
+    up: object
+    up_scales: object
+    down: object
+    down_scales: object
+
+    @property
+    def E(self) -> int:
+        return int(self.gate.shape[0])
+
+    @property
+    def f(self) -> int:
+        return int(self.gate.shape[1])
+
+    def c(self, d: int) -> moe_fp8_experts:
+        torch = _torch()
+        E, f = self.E, self.f
+        out = moe_fp8_experts()
+        for name, n, K in (("gate", f, d), ("up", f, d), ("down", d, f)):
+            setattr(out, name, _codes(getattr(self, name), (E, n, K), name))
+            setattr(out, name + "_scales", _sized(getattr(self, name + "_scales"), (E, _runs(n), _runs(K)),
+                                                  torch.float32, name + "_scales"))
+        return out
+
+
+def alloc_workspace_fp8(shape: Shape, device="cuda", stream=None):
+    """A workspace tensor of moe_layer_fp8 for `shape` (header cleared)."""
+    torch = _torch()
+    n = int(lib().moe_layer_fp8_workspace_bytes(ctypes.byref(shape.c())))
+    if n == 0:
+        raise MoeError(MOE_ERR_SHAPE, "alloc_workspace_fp8")
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    moe_workspace_init(ws, stream)
+    return ws
+
+
+def layer_fp8(x, xq, xq_scales, experts: ExpertsFp8, k: int, *, w_router=None, bias=None, logits=None, ws=None,
+              stream=None, check: bool = False):
+    """moe_layer_fp8: the layer with FP8 experts on the outputs of one
+    add_rmsnorm (x bf16 for the router, xq and xq_scales for the experts);
+    returns (out, topk_ids, topk_w, logits)."""
+    torch = _torch()
+    T, d = xq.shape
+    E = experts.E
+    shape = Shape(T, d, E, k, experts.f)
+    xp = None if x is None else _sized(x, (T, d), torch.bfloat16, "x")
+    xqp = _codes(xq, (T, d), "xq")
+    xsp = _sized(xq_scales, (T, _runs(d)), torch.float32, "xq_scales")
+    wrp = None if w_router is None else _sized(w_router, (E, d), torch.float32, "w_router")
+    bp = None if bias is None else _sized(bias, (E,), torch.float32, "bias")
+    ex, cs = experts.c(d), shape.c()
+    with _scope("layer_fp8", stream, xq, x, xq_scales, w_router, bias, logits, ws,
+                *(getattr(experts, n) for n, _ in moe_fp8_experts._fields_)):
+        dev = xq.device
+        if logits is None:
+            logits = torch.empty((T, E), dtype=torch.float32, device=dev)
+        ids = torch.empty((T, k), dtype=torch.int32, device=dev)
+        w = torch.empty((T, k), dtype=torch.float32, device=dev)
+        out = torch.empty((T, d), dtype=torch.float32, device=dev)
+        if ws is None:
+            ws = alloc_workspace_fp8(shape, dev)
+        _call("moe_layer_fp8", ctypes.byref(cs), xp, xqp, xsp, wrp, bp,
+              _sized(logits, (T, E), torch.float32, "logits"), ctypes.byref(ex), ids.data_ptr(), w.data_ptr(),
+              out.data_ptr(), _ptr(ws, name="ws"), ws.numel() * ws.element_size())
+        if check:
+            check_device_status(ws, "layer_fp8")
     return out, ids, w, logits
 
 
