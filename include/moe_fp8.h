@@ -94,8 +94,8 @@ int moe_add_rmsnorm(int32_t T, int32_t d, const void* x, int32_t x_type, int64_t
    fp32.  bf16 results of large products use the fp8 matrix instructions,
    which align the products of a step of 128 before adding them: about 1.5e-5
    relative on normal values, at most 2^-9 of the step's largest product.
-   Limits: M >= 0 (0 enqueues nothing), N >= 1, K a positive multiple of 32;
-   M, N, K < 2^30.  Errors: MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_ERR_FORMAT,
+   Limits: M >= 0 (0 enqueues nothing), N >= 1, both below 2^30; K a positive
+   multiple of 32 up to 2^22.  Errors: MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_ERR_FORMAT,
    MOE_ERR_ALIGN, MOE_ERR_HIP. */
 int moe_gemm_fp8(int32_t M, int32_t N, int32_t K, const uint8_t* a, int64_t a_stride, const float* a_scales,
                  const uint8_t* w, const float* w_scales, void* out, int32_t out_type, int64_t out_stride,
@@ -131,7 +131,8 @@ int moe_grouped_gemm_fp8(int32_t R, int32_t E, int32_t N, int32_t K, const uint8
    moe_add_rmsnorm.  Rows at or past offsets[E] are left as they were.
    ws: moe_expert_gate_up_fp8_workspace_bytes(shape) bytes (0: ws may be
    NULL), uninitialised; one call at a time.  Limits as include/moe.h
-   (moe_shape), offsets and perm clamped as above.  Errors: as
+   (moe_shape) with d <= 2^22 (and f, in moe_layer_fp8), offsets and perm
+   clamped as above.  Errors: as
    moe_expert_ffn. */
 size_t moe_expert_gate_up_fp8_workspace_bytes(const moe_shape* shape);
 int moe_expert_gate_up_fp8(const moe_shape* shape, const uint8_t* a, const float* a_scales, const uint8_t* gate,

@@ -18,10 +18,11 @@ int hip_rc(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_HIP; }
 bool known_type(int t) { return t == MOE_TYPE_BF16 || t == MOE_TYPE_F32; }
 
 constexpr int kDimLimit = 1 << 30;
+constexpr int kDepthLimit = 1 << 22;      // 256 weight rows within a 32-bit offset
 
 // Sizes of one product: N weight rows of depth K.
 int check_dims(int N, int K) {
-    if (N < 1 || N >= kDimLimit || K < 32 || K % 32 || K >= kDimLimit) return MOE_ERR_SHAPE;
+    if (N < 1 || N >= kDimLimit || K < 32 || K % 32 || K > kDepthLimit) return MOE_ERR_SHAPE;
     return MOE_OK;
 }
 
@@ -106,6 +107,7 @@ int check_gate_up(const moe_shape& s, const uint8_t* a, const float* a_scales, c
                   const float* gate_scales, const uint8_t* up, const float* up_scales, const int32_t* offsets,
                   const int32_t* perm, const uint8_t* act, const float* act_scales, const void* ws, size_t ws_bytes) {
     int rc;
+    if ((rc = check_dims(s.f, s.d)) != MOE_OK) return rc;
     if ((rc = check_operands(a, a_scales, gate, gate_scales)) != MOE_OK) return rc;
     if ((rc = check_operands(a, a_scales, up, up_scales)) != MOE_OK) return rc;
     if (!offsets || !perm || !act || !act_scales) return MOE_ERR_NULL;
@@ -237,6 +239,7 @@ int moe_layer_fp8(const moe_shape* shape, const uint16_t* x, const uint8_t* xq, 
     if ((rc = check_gate_up(s, xq, xq_scales, ex.gate, ex.gate_scales, ex.up, ex.up_scales, offsets, perm, act,
                             act_scales, base + c.hidden, hidden_bytes(s))) != MOE_OK)
         return rc;
+    if ((rc = check_dims(s.d, s.f)) != MOE_OK) return rc;
     if ((rc = check_operands(act, act_scales, ex.down, ex.down_scales)) != MOE_OK) return rc;
 
     if (small_route_supported(s)) {

@@ -43,7 +43,7 @@ struct RowItem {
 __device__ __forceinline__ RowItem row_item(const Fp8Args& a, int idx, int rows) {
     if (!a.offsets) {
         const int r0 = idx * rows;
-        return RowItem{0, r0, min(a.R, r0 + rows)};
+        return RowItem{r0 < a.R ? 0 : -1, r0, min(a.R, r0 + rows)};
     }
     const int lane = threadIdx.x & 63;
     int lo = 0, hi = 0;
@@ -111,7 +111,7 @@ __device__ __forceinline__ float run_scale(float amax) { return fmaxf(amax / kE4
 // Output columns of one workgroup of the many-row kernel.
 constexpr int fp8_tile_cols(bool gate_up) { return gate_up ? 128 : 256; }
 // Token rows (in 16s) of one workgroup of the many-row kernel.
-inline int fp8_tile_rows16(const Fp8Args& a, bool gate_up) { return gate_up || a.out_f32 ? 4 : 8; }
+inline int fp8_tile_rows16(const Fp8Args& a, bool gate_up) { return 8; }
 
 // Rows an expert has on average when every expert that can have rows has some.
 inline int fp8_mean_rows(const Fp8Args& a) {
@@ -132,7 +132,7 @@ inline bool fp8_uses_skinny(const Fp8Args& a) { return fp8_mean_rows(a) <= (a.of
 inline long long fp8_blocks(const Fp8Args& a, bool gate_up) {
     if (fp8_uses_skinny(a)) return static_cast<long long>((a.N + 15) / 16) * row_items(a, 16 * fp8_skinny_rows16(a));
     const int cols = fp8_tile_cols(gate_up);
-    return static_cast<long long>((a.N + cols - 1) / cols) * row_items(a, 16 * fp8_tile_rows16(a, gate_up));
+    return static_cast<long long>((a.N + cols - 1) / cols) * ((row_items(a, 16 * fp8_tile_rows16(a, gate_up)) + 7) / 8 * 8);
 }
 
 hipError_t launch_fp8_skinny(const Fp8Args& a, bool gate_up, hipStream_t st);

@@ -6,18 +6,27 @@
 // one fp32 multiply-add per output and step adds them, scaled, to the
 // accumulators.
 //
-// A workgroup of four waves computes 256 weight rows x 16*MT token rows; wave
-// w owns 64 weight rows (gate/up: 32 gate rows and the same 32 up rows), so
-// no two waves need the same weights and each wave loads its own straight
-// from memory into the matrix operand, one step ahead.  The token rows are
-// shared: they are staged in LDS, two buffers, swizzled so that the 16 rows
-// of a fragment read start in distinct banks.
+// A workgroup of eight waves computes 256 weight rows (gate/up: 128 gate rows
+// and the same 128 up rows) x up to 128 token rows of one expert.  Both
+// operands go from memory to LDS as they are, by direct copies of 16 bytes a
+// lane, into a ring of stages of one step each: eight neighbouring lanes take
+// one row's 128 bytes, whole cache lines.  (Loading the matrix operands
+// straight into registers, lane = row, asks for 16 bytes of another line in
+// every lane; that path stopped at 6 TB/s from the caches, whatever the
+// prefetch distance.)  The 16-byte chunks of a row are stored XOR-swizzled by
+// (row / 2) mod 8, so the 16 rows of a fragment read lie in distinct banks.
+//
+// The waves split the tile by its live rows: 4 x 2 waves of 64 weight rows x
+// 64 token rows above 64 rows, else 8 waves of 32 weight rows x all token
+// rows (64, 32 or 16), whose smaller stages leave room for a deeper ring.
 //
 // FAST: operands stay E4M3 on the 16x16x128 fp8 instruction, whose internal
 // alignment costs about 1.5e-5 relative per step (measured on normal values);
-// used for bf16 results only.  Otherwise operands are converted to bf16
+// used for bf16 results only.  Otherwise fragments are converted to bf16
 // (exact) and the products run on the 16x16x32 bf16 instruction at half the
 // rate, with fp32 accuracy.
+#include <type_traits>
+
 #include "fp8.hpp"
 #include "kernels.hpp"
 
@@ -26,27 +35,63 @@ namespace qrmoe {
 namespace {
 
 constexpr int kTileN = 256;
-constexpr int kTileThreads = 256;
+constexpr int kTileM = 128;
+constexpr int kTileWaves = 8;
+constexpr int kTileThreads = kTileWaves * kWave;
+constexpr int kWBytes = kTileN * kRun;              // weights of a stage
 
-template <bool FAST> constexpr int kRowBytes = FAST ? 128 : 256;
+// WM: waves along the token rows, TT: 16-row token tiles of a wave.
+template <int WM, int TT> struct Shape {
+    static constexpr int rows = 16 * TT * WM;       // token rows of a stage
+    static constexpr int wn = kTileWaves / WM;      // waves along the weight rows
+    static constexpr int frags = 2 * WM;            // 16-row weight fragments of a wave
+    static constexpr int stage = kWBytes + rows * kRun + 512;     // weights, tokens, token scales
+    static constexpr int ring = rows >= 64 ? 3 : 4;
+    // copies of a wave per stage: weights, tokens (1 KB each), token scales
+    static constexpr int tcopies = rows > 64 ? 2 : 1;
+    static constexpr int loads = 4 + tcopies + 1;
+};
+constexpr int kTileLds = 149504;
+static_assert(Shape<2, 4>::stage * Shape<2, 4>::ring <= kTileLds && Shape<1, 4>::stage * Shape<1, 4>::ring <= kTileLds &&
+                  Shape<1, 2>::stage * Shape<1, 2>::ring <= kTileLds && Shape<1, 1>::stage * Shape<1, 1>::ring <= kTileLds,
+              "stage ring");
 
-// LDS offset of 16-byte chunk c of token row r.  E4M3 rows of 128 bytes (8
-// chunks): two rows span the 64 banks, so rows 2i and 2i+1 share a key; bf16
-// rows of 256 bytes (16 chunks).
-template <bool FAST>
-__device__ __forceinline__ int swz(int r, int c) {
-    if constexpr (FAST) return r * 128 + ((c ^ ((r >> 1) & 7)) << 4);
-    else return r * 256 + ((c ^ (r & 15)) << 4);
+// Memory from p on, for copies by a 32-bit lane offset and a scalar offset
+// (raw 32-bit data, no stride; every offset is inside the tensor).
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const uint8_t* p) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p), 0, 0xffffffffu, 4 << 15);
 }
 
-__device__ __forceinline__ u32x4 load_chunk(const uint8_t* row, int k, int K) {
-    const bool in = k < K;      // K is a multiple of 32: a chunk is inside or outside
-    const u32x4 v = *reinterpret_cast<const u32x4*>(row + (in ? k : 0));
-    return in ? v : u32x4{0u, 0u, 0u, 0u};
+// Floats that no kernel writes while this one runs, read through the scalar
+// cache: a wave's block scales are one value for all lanes.
+typedef const __attribute__((address_space(4))) float Scalar;
+__device__ __forceinline__ Scalar* scalar_ptr(const float* p) {
+    return reinterpret_cast<Scalar*>(reinterpret_cast<uintptr_t>(p));
 }
 
-template <bool FAST> struct WOp;
-template <> struct WOp<true> {
+// At most r (<= R) stages of L copies each are still in flight.
+template <int L, int R>
+__device__ __forceinline__ void wait_stages(int r) {
+    if constexpr (R == 0) {
+        wait_vmcnt<0>();
+    } else {
+        if (r >= R) wait_vmcnt<R * L>();
+        else wait_stages<L, R - 1>(r);
+    }
+}
+
+// Every wave has finished its LDS reads and the copies it waited for; no
+// LDS access moves across.
+__device__ __forceinline__ void stage_barrier() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// A fragment's operand: chunks l/16 and 4 + l/16 of row l%16 (K is permuted
+// inside the step by that choice, the same for weights and tokens).
+template <bool FAST> struct Operand;
+template <> struct Operand<true> {
     i32x8 v;
     __device__ __forceinline__ void set(u32x4 lo, u32x4 hi) {
 #pragma unroll
@@ -56,7 +101,7 @@ template <> struct WOp<true> {
         }
     }
 };
-template <> struct WOp<false> {
+template <> struct Operand<false> {
     bf16x8 v[4];
     __device__ __forceinline__ void set(u32x4 lo, u32x4 hi) {
         v[0] = e4m3x8_to_bf16(lo[0], lo[1]);
@@ -66,131 +111,187 @@ template <> struct WOp<false> {
     }
 };
 
-__device__ __forceinline__ f32x4 step_product(const WOp<true>& w, const WOp<true>& t) {
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w.v, t.v, f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
-}
-__device__ __forceinline__ f32x4 step_product(const WOp<false>& w, const WOp<false>& t) {
-    f32x4 p = {0.f, 0.f, 0.f, 0.f};
+// The step's products of a wave's weight fragments and one token tile.
+template <int F>
+__device__ __forceinline__ void step_products(const Operand<true> (&w)[F], const Operand<true>& t, f32x4 (&p)[F]) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) p = mfma16x16x32(w.v[j], t.v[j], p);
-    return p;
+    for (int f = 0; f < F; ++f)
+        p[f] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w[f].v, t.v, f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
+}
+template <int F>
+__device__ __forceinline__ void step_products(const Operand<false> (&w)[F], const Operand<false>& t, f32x4 (&p)[F]) {
+#pragma unroll
+    for (int f = 0; f < F; ++f) p[f] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int f = 0; f < F; ++f) p[f] = mfma16x16x32(w[f].v[j], t.v[j], p[f]);
 }
 
-// GU: gate/up with SwiGLU and E4M3 output, 128 columns of act per workgroup.
-template <int MT, bool GU, bool FAST>
-__global__ __launch_bounds__(kTileThreads, 2) void fp8_tile_kernel(Fp8Args a, int n_tiles) {
-    constexpr int kRows = 16 * MT;
+// One workgroup's product.  GU: gate/up with SwiGLU and E4M3 output.
+template <int WM, int TT, bool GU, bool FAST>
+__device__ __forceinline__ void tile_body(const Fp8Args& a, const RowItem& it, int n_tile, uint8_t* lds) {
+    using H = Shape<WM, TT>;
+    constexpr int F = H::frags, NST = H::ring, SB = H::stage, L = H::loads;
     constexpr int kCols = GU ? kTileN / 2 : kTileN;     // output columns
-    constexpr int kChunks = kRows * 8 / kTileThreads;   // 16-byte token chunks a thread stages per step
-    __shared__ __align__(16) uint8_t tok[2][kRows * kRowBytes<FAST>];
-    __shared__ float tscale[2][kRows];
-    __shared__ float rowmax[GU ? 4 : 1][GU ? kRows : 1];
+    constexpr int kMats = GU ? 2 : 1;
 
     const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, col = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int n_tile = blockIdx.x % n_tiles, item = blockIdx.x / n_tiles;
+    const int wn = wave & (H::wn - 1), wm = wave / H::wn;
     const int n0 = n_tile * kCols;
-    if constexpr (!GU)
-        if (a.offsets && item == 0) zero_rows_past_end(a, n0, min(n0 + kCols, a.N));
-    const RowItem it = row_item(a, item, kRows);
-    if (it.e < 0) return;
     const int S = ceil_div(a.K, kRun), NB = ceil_div(a.N, kRun);
+    const int full = a.K / kRun;                        // whole steps
+    // Rows of K bytes put the same step of all rows on few memory channels
+    // (256 bytes apart, repeating every 4 KB): the column tiles start their
+    // sums at steps spread over K.  The order depends on the column only.
+    const int rot = full ? static_cast<int>(static_cast<long long>(n_tile) * full / ceil_div(a.N, kCols)) % full : 0;
+    // the i-th step in this column tile's order; the partial step comes last
+    auto nth = [&](int i) {
+        const int s = i + rot;
+        return i >= full ? i : s < full ? s : s - full;
+    };
 
-    // this wave's four 16-row weight fragments
-    const uint8_t* wrow[4];
-    const float* wscale[4];
-    int wn[4];                                          // first output column of the fragment
+    // ---- copies: weight rows 32 wave + 8 i + lane/8 of the tile (gate/up:
+    // waves 0-3 gate, 4-7 up), position lane%8 of the row in LDS holding chunk
+    // (lane%8) ^ (row/2)%8
+    const int mat = GU ? wave >> 2 : 0;
+    const __amdgpu_buffer_rsrc_t wbuf = buffer_of(a.w[mat] + (static_cast<size_t>(it.e) * a.N + n0) * a.K);
+    const int chunk0 = (lane & 7) ^ (lane >> 4);        // rows of even 8 i; of odd 8 i: chunk0 ^ 4
+    int woff[4];
 #pragma unroll
-    for (int f = 0; f < 4; ++f) {
-        const int m = GU ? f >> 1 : 0;
-        wn[f] = GU ? n0 + 32 * wave + 16 * (f & 1) : n0 + 64 * wave + 16 * f;
-        const int row = min(wn[f] + col, a.N - 1);
-        wrow[f] = a.w[m] + (static_cast<size_t>(it.e) * a.N + row) * a.K;
-        wscale[f] = a.w_scales[m] + (static_cast<size_t>(it.e) * NB + min(wn[f], a.N - 1) / kRun) * S;
+    for (int i = 0; i < 4; ++i) {
+        const int row = (GU ? 32 * (wave & 3) : 32 * wave) + 8 * i + (lane >> 3);
+        woff[i] = min(row, a.N - 1 - n0) * a.K + 16 * (chunk0 ^ (4 * (i & 1)));     // at most 256 * 2^22
     }
-    // the token chunks this thread stages: chunk tid%8 of rows tid/8 + 32 i
-    const uint8_t* trow[kChunks];
+    // token rows: the wave's share of the stage's rows, tcopies times 8 (64
+    // rows or more) or fewer rows in the low lanes
+    constexpr int kShare = H::rows / kTileWaves;        // rows of a wave: 16, 8, 4 or 2
+    const uint8_t* tsrc[H::tcopies];
 #pragma unroll
-    for (int i = 0; i < kChunks; ++i)
-        trow[i] = a.a + source_row(a, min(it.r0 + tid / 8 + 32 * i, it.r1 - 1)) * a.a_stride;
-    const float* trow_scale = a.a_scales + static_cast<size_t>(source_row(a, min(it.r0 + min(tid, kRows - 1), it.r1 - 1))) * S;
-
-    u32x4 wnext[4][2], tnext[kChunks];
-    float snext;
-    auto fetch = [&](int s) {
+    for (int i = 0; i < H::tcopies; ++i) {
+        const int row = kShare * wave + 8 * i + (lane >> 3);
+        tsrc[i] = a.a + source_row(a, min(it.r0 + row, it.r1 - 1)) * a.a_stride + 16 * ((lane & 7) ^ ((row >> 1) & 7));
+    }
+    const float* ssrc = a.a_scales + static_cast<size_t>(source_row(a, min(it.r0 + kShare * wave + (lane & 15), it.r1 - 1))) * S;
+    auto issue = [&](int i) {
+        uint8_t* base = lds + (i % NST) * SB;
+        const int s = nth(i);
+        // the partial step: a chunk past K is read from the step's start (and
+        // cleared when it is used)
+        const int part = s == full ? -1 : 0;
 #pragma unroll
-        for (int f = 0; f < 4; ++f)
+        for (int c = 0; c < 4; ++c) {
+            const int k = 16 * (chunk0 ^ (4 * (c & 1)));
+            const int back = (full * kRun + k < a.K ? 0 : k) & part;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(wbuf, (lds_void*)(base + (32 * wave + 8 * c) * kRun), 16, woff[c] - back,
+                                                     s * kRun, 0, 0);
+        }
 #pragma unroll
-            for (int h = 0; h < 2; ++h) wnext[f][h] = load_chunk(wrow[f], s * kRun + 64 * h + 16 * g, a.K);
-#pragma unroll
-        for (int i = 0; i < kChunks; ++i) tnext[i] = load_chunk(trow[i], s * kRun + 16 * (tid & 7), a.K);
-        snext = trow_scale[s];
+        for (int c = 0; c < H::tcopies; ++c) {
+            const int k = 16 * ((lane & 7) ^ (((kShare * wave + 8 * c + (lane >> 3)) >> 1) & 7));
+            const int back = (full * kRun + k < a.K ? 0 : k) & part;
+            if (kShare >= 8 || lane < 8 * kShare)
+                __builtin_amdgcn_global_load_lds(tsrc[c] + (s * kRun - back), (lds_void*)(base + kWBytes + (kShare * wave + 8 * c) * kRun),
+                                                 16, 0, 0);
+        }
+        if (lane < kShare)
+            __builtin_amdgcn_global_load_lds(ssrc + s, (lds_void*)(base + kWBytes + H::rows * kRun + 4 * kShare * wave), 4, 0, 0);
     };
-    auto stage = [&](int buf) {
+
+    // ---- this wave's fragments: weight rows of the tile and output columns
+    int wrow[F], wcol[F];
+    Scalar* wscale[kMats];
 #pragma unroll
-        for (int i = 0; i < kChunks; ++i) {
-            const int r = tid / 8 + 32 * i, c = tid & 7;
-            if constexpr (FAST) {
-                *reinterpret_cast<u32x4*>(&tok[buf][swz<true>(r, c)]) = tnext[i];
-            } else {
-                *reinterpret_cast<bf16x8*>(&tok[buf][swz<false>(r, 2 * c)]) = e4m3x8_to_bf16(tnext[i][0], tnext[i][1]);
-                *reinterpret_cast<bf16x8*>(&tok[buf][swz<false>(r, 2 * c + 1)]) = e4m3x8_to_bf16(tnext[i][2], tnext[i][3]);
-            }
-        }
-        if (tid < kRows) tscale[buf][tid] = snext;
+    for (int f = 0; f < F; ++f) {
+        const int c = GU ? 16 * WM * wn + 16 * (f % WM) : 16 * F * wn + 16 * f;
+        wrow[f] = GU ? 128 * (f / WM) + c : c;
+        wcol[f] = n0 + c;
+    }
+#pragma unroll
+    for (int m = 0; m < kMats; ++m)      // a wave's columns share a block of 128
+        wscale[m] = scalar_ptr(a.w_scales[m] + (static_cast<size_t>(it.e) * NB + min(wcol[0], a.N - 1) / kRun) * S);
+    // chunk l/16 of row l%16; chunk 4 + l/16 is at the offset ^ 64
+    const int frag = col * kRun + ((g ^ (col >> 1)) << 4);
+
+    f32x4 acc[F][TT];
+#pragma unroll
+    for (int f = 0; f < F; ++f)
+#pragma unroll
+        for (int t = 0; t < TT; ++t) acc[f][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    float ws[kMats];
+    auto load_ws = [&](int s) {
+#pragma unroll
+        for (int m = 0; m < kMats; ++m) ws[m] = wscale[m][s];
     };
 
-    f32x4 acc[4][MT];
+    auto multiply = [&](int i, auto partial) {
+        const uint8_t* base = lds + (i % NST) * SB;
+        const uint8_t* lo = base + frag;
+        const uint8_t* hi = base + (frag ^ 64);
+        const uint8_t* tlo = lo + kWBytes + 16 * TT * wm * kRun;
+        const uint8_t* thi = hi + kWBytes + 16 * TT * wm * kRun;
+        const float* ts = reinterpret_cast<const float*>(base + kWBytes + H::rows * kRun) + 16 * TT * wm + col;
+        auto operand = [&](Operand<FAST>& o, const uint8_t* l, const uint8_t* h) {
+            u32x4 c0 = *reinterpret_cast<const u32x4*>(l), c1 = *reinterpret_cast<const u32x4*>(h);
+            if constexpr (partial) {
+                if (full * kRun + 16 * g >= a.K) c0 = u32x4{0u, 0u, 0u, 0u};
+                if (full * kRun + 64 + 16 * g >= a.K) c1 = u32x4{0u, 0u, 0u, 0u};
+            }
+            o.set(c0, c1);
+        };
+        float w[kMats];
 #pragma unroll
-    for (int f = 0; f < 4; ++f)
+        for (int m = 0; m < kMats; ++m) w[m] = ws[m];
+        Operand<FAST> wo[F];
 #pragma unroll
-        for (int t = 0; t < MT; ++t) acc[f][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int f = 0; f < F; ++f) operand(wo[f], lo + wrow[f] * kRun, hi + wrow[f] * kRun);
+        if (!partial) load_ws(nth(min(i + 1, S - 1)));
+#pragma unroll
+        for (int t = 0; t < TT; ++t) {
+            Operand<FAST> to;
+            operand(to, tlo + 16 * t * kRun, thi + 16 * t * kRun);
+            f32x4 p[F];
+            step_products(wo, to, p);
+            const float s = ts[16 * t];
+#pragma unroll
+            for (int f = 0; f < F; ++f) {
+                const float m = s * w[GU ? f / WM : 0];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) acc[f][t][q] = fmaf(p[f][q], m, acc[f][t][q]);
+            }
+        }
+    };
 
-    fetch(0);
-    stage(0);
-    for (int s = 0; s < S; ++s) {
-        WOp<FAST> wo[4];
-        float ws[4];
-#pragma unroll
-        for (int f = 0; f < 4; ++f) {
-            wo[f].set(wnext[f][0], wnext[f][1]);
-            ws[f] = wscale[f][s];
-        }
-        __syncthreads();
-        if (s + 1 < S) fetch(s + 1);
-        const uint8_t* buf = tok[s & 1];
-#pragma unroll
-        for (int t = 0; t < MT; ++t) {
-            const int r = 16 * t + col;
-            WOp<FAST> to;
-            if constexpr (FAST) {
-                to.set(*reinterpret_cast<const u32x4*>(&buf[swz<true>(r, g)]),
-                       *reinterpret_cast<const u32x4*>(&buf[swz<true>(r, 4 + g)]));
-            } else {
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    to.v[j] = *reinterpret_cast<const bf16x8*>(&buf[swz<false>(r, (j >> 1) * 8 + 2 * g + (j & 1))]);
-            }
-            const float ts = tscale[s & 1][r];
-#pragma unroll
-            for (int f = 0; f < 4; ++f) {
-                const f32x4 p = step_product(wo[f], to);
-                const float m = ts * ws[f];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) acc[f][t][i] = fmaf(p[i], m, acc[f][t][i]);
-            }
-        }
-        if (s + 1 < S) stage((s + 1) & 1);
+    load_ws(nth(0));
+    for (int i = 0; i < NST - 1 && i < S; ++i) issue(i);
+    // Step i: its copies have arrived (all but the younger stages'), every
+    // wave is past step i - 1, whose buffer stage i + NST - 1 then takes.
+    auto begin = [&](int i) {
+        const int younger = min(S - 1, i + NST - 2) - i;
+        if (younger == NST - 2) wait_vmcnt<L * (NST - 2)>();
+        else wait_stages<L, NST - 2>(younger);
+        stage_barrier();
+        if (i + NST - 1 < S) issue(i + NST - 1);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    for (int i = 0; i < full; ++i) {
+        begin(i);
+        multiply(i, std::false_type{});
+    }
+    if (full < S) {
+        begin(full);
+        multiply(full, std::true_type{});
     }
 
     if constexpr (!GU) {
 #pragma unroll
-        for (int t = 0; t < MT; ++t) {
-            const int r = it.r0 + 16 * t + col;
+        for (int t = 0; t < TT; ++t) {
+            const int r = it.r0 + 16 * (TT * wm + t) + col;
             if (r >= it.r1) continue;
 #pragma unroll
-            for (int f = 0; f < 4; ++f) {
-                const int n = wn[f] + 4 * g;
+            for (int f = 0; f < F; ++f) {
+                const int n = wcol[f] + 4 * g;
                 const long long at = r * a.out_stride + n;
                 const f32x4 v = acc[f][t];
                 if (a.out_vec && n + 4 <= a.N) {
@@ -211,38 +312,62 @@ __global__ __launch_bounds__(kTileThreads, 2) void fp8_tile_kernel(Fp8Args a, in
         }
     } else {
         // v = silu(g) u in place of the gate accumulators; a run's 128
-        // columns are the workgroup's, 8 per lane and token
-        const bool in = wn[0] < a.N;        // f is a multiple of 32: a wave's columns are inside or outside
+        // columns are the workgroup's, 4 WM per lane and token
+        float* rowmax = reinterpret_cast<float*>(lds);
+        __syncthreads();
 #pragma unroll
-        for (int t = 0; t < MT; ++t) {
+        for (int t = 0; t < TT; ++t) {
             float m = 0.f;
 #pragma unroll
-            for (int f = 0; f < 2; ++f)
+            for (int f = 0; f < WM; ++f)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    acc[f][t][i] = in ? silu_mul(acc[f][t][i], acc[2 + f][t][i]) : 0.f;
+                    // f is a multiple of 32, so a fragment is inside or outside
+                    acc[f][t][i] = wcol[f] < a.N ? silu_mul(acc[f][t][i], acc[WM + f][t][i]) : 0.f;
                     m = fmaxf(m, fabsf(acc[f][t][i]));
                 }
             m = fmaxf(m, __shfl_xor(m, 16));
             m = fmaxf(m, __shfl_xor(m, 32));
-            if (g == 0) rowmax[wave][16 * t + col] = m;
+            if (g == 0) rowmax[wn * H::rows + 16 * (TT * wm + t) + col] = m;
         }
         __syncthreads();
 #pragma unroll
-        for (int t = 0; t < MT; ++t) {
-            const int rt = 16 * t + col, r = it.r0 + rt;
+        for (int t = 0; t < TT; ++t) {
+            const int rt = 16 * (TT * wm + t) + col, r = it.r0 + rt;
             if (r >= it.r1) continue;
-            const float s = run_scale(fmaxf(fmaxf(rowmax[0][rt], rowmax[1][rt]), fmaxf(rowmax[2][rt], rowmax[3][rt])));
-            if (wave == 0 && g == 0) a.act_scales[static_cast<size_t>(r) * NB + n_tile] = s;
-            if (!in) continue;
+            float m = rowmax[rt];
 #pragma unroll
-            for (int f = 0; f < 2; ++f) {
+            for (int w = 1; w < H::wn; ++w) m = fmaxf(m, rowmax[w * H::rows + rt]);
+            const float s = run_scale(m);
+            if (wn == 0 && g == 0) a.act_scales[static_cast<size_t>(r) * NB + n_tile] = s;
+#pragma unroll
+            for (int f = 0; f < WM; ++f) {
                 const f32x4 v = acc[f][t];
-                *reinterpret_cast<uint32_t*>(a.act + static_cast<size_t>(r) * a.N + wn[f] + 4 * g) =
-                    e4m3x4_rne(v[0] / s, v[1] / s, v[2] / s, v[3] / s);
+                if (wcol[f] < a.N)
+                    *reinterpret_cast<uint32_t*>(a.act + static_cast<size_t>(r) * a.N + wcol[f] + 4 * g) =
+                        e4m3x4_rne(v[0] / s, v[1] / s, v[2] / s, v[3] / s);
             }
         }
     }
+}
+
+template <bool GU, bool FAST>
+__global__ __launch_bounds__(kTileThreads, 2) void fp8_tile_kernel(Fp8Args a, int n_tiles) {
+    __shared__ __align__(256) uint8_t lds[kTileLds];
+    // workgroup ids go round the 8 XCDs: an XCD takes all column tiles of an item
+    const int xcd = blockIdx.x % 8, at = blockIdx.x / 8;
+    const int n_tile = at % n_tiles, item = at / n_tiles * 8 + xcd;
+    if constexpr (!GU) {
+        const int n0 = n_tile * kTileN;
+        if (a.offsets && item == 0) zero_rows_past_end(a, n0, min(n0 + kTileN, a.N));
+    }
+    const RowItem it = row_item(a, item, kTileM);
+    if (it.e < 0) return;
+    const int rows = __builtin_amdgcn_readfirstlane(it.r1 - it.r0);
+    if (rows > 64) tile_body<2, 4, GU, FAST>(a, it, n_tile, lds);
+    else if (rows > 32) tile_body<1, 4, GU, FAST>(a, it, n_tile, lds);
+    else if (rows > 16) tile_body<1, 2, GU, FAST>(a, it, n_tile, lds);
+    else tile_body<1, 1, GU, FAST>(a, it, n_tile, lds);
 }
 
 }  // namespace
@@ -250,9 +375,9 @@ __global__ __launch_bounds__(kTileThreads, 2) void fp8_tile_kernel(Fp8Args a, in
 hipError_t launch_fp8_tile(const Fp8Args& a, bool gate_up, hipStream_t st) {
     const int n_tiles = ceil_div(a.N, fp8_tile_cols(gate_up));
     const int blocks = static_cast<int>(fp8_blocks(a, gate_up));
-    if (gate_up) fp8_tile_kernel<4, true, false><<<blocks, kTileThreads, 0, st>>>(a, n_tiles);
-    else if (a.out_f32) fp8_tile_kernel<4, false, false><<<blocks, kTileThreads, 0, st>>>(a, n_tiles);
-    else fp8_tile_kernel<8, false, true><<<blocks, kTileThreads, 0, st>>>(a, n_tiles);
+    if (gate_up) fp8_tile_kernel<true, false><<<blocks, kTileThreads, 0, st>>>(a, n_tiles);
+    else if (a.out_f32) fp8_tile_kernel<false, false><<<blocks, kTileThreads, 0, st>>>(a, n_tiles);
+    else fp8_tile_kernel<false, true><<<blocks, kTileThreads, 0, st>>>(a, n_tiles);
     return hipGetLastError();
 }
 
