@@ -181,9 +181,15 @@ def status_str(code: int) -> str:
 
 # ------------------------------------------------------------------ helpers
 
+_TORCH = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _TORCH
+    if _TORCH is None:
+        import torch
+        _TORCH = torch
+    return _TORCH
 
 
 def _stream(stream) -> int:
@@ -642,20 +648,36 @@ def layer_shared(x, experts: Experts, shared: Experts, k: int, *, w_router=None,
 
 # -------------------------------------------------------------- FP8 operators
 
-def _codes(t, shape, name):
-    """Address of E4M3 codes (float8_e4m3fn or uint8) of the given shape."""
-    torch = _torch()
-    p = _ptr(t, (torch.float8_e4m3fn, torch.uint8), name)
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
-    return p
+# The smallest of these calls run a few microseconds on the GPU, less than a
+# call through Python takes by default, so their checks are written for it: one
+# test per tensor, the reason looked for only when it fails.
+
+def _addr(t, dtypes, shape, dev, name):
+    """Address of a contiguous tensor of `shape` on device number `dev`, its
+    dtype one of `dtypes`."""
+    if t.dtype in dtypes and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected {' or '.join(map(str, dtypes))}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, not on device {dev}")
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _sized(t, shape, dtype, name):
-    p = _ptr(t, dtype, name)
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
-    return p
+def _rows(t, dev, name):
+    """(address, values from row to row) of a 2-D tensor on device number
+    `dev` whose rows are contiguous but may lie apart."""
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, not on device {dev}")
+    rows, n = t.shape
+    stride, step = t.stride()
+    if step != 1 and n > 1:
+        raise ValueError(f"{name}'s rows must be contiguous")
+    return t.data_ptr(), stride if rows > 1 else n
 
 
 def _runs(n: int) -> int:
@@ -672,39 +694,32 @@ def _moe_type(dtype, name: str) -> int:
     raise ValueError(f"{name} has dtype {dtype}, expected torch.bfloat16 or torch.float32")
 
 
-def _rows(t, name: str):
-    """(address, stride in values) of a 2-D device tensor whose rows are
-    contiguous (they may lie apart)."""
-    if t.dim() != 2:
-        raise ValueError(f"{name} must have two dimensions")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a device tensor")
-    if t.shape[1] > 1 and t.stride(1) != 1:
-        raise ValueError(f"{name}'s rows must be contiguous")
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
-
-
-def _scope(name: str, stream, first, *others):
-    """The scope of a call on the device of `first`, on `stream` (default: the
-    current stream of that device): inside it the device and the stream are
-    the current ones, so that what the call allocates belongs to the stream
-    that uses it."""
+def _elsewhere(dev, stream, where: str):
+    """None when a call on device number `dev` can go to the current stream,
+    else the scope (of that device, and of `stream` if given) to make it in:
+    what the call allocates then belongs to the stream that uses it."""
     torch = _torch()
-    dev = first.device
-    if dev.type != "cuda":
-        raise ValueError(f"{name} takes device tensors")
-    for t in others:
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name}: tensors on {dev} and {t.device}")
+    if dev < 0:
+        raise ValueError(f"{where} takes device tensors")
     if stream is not None:
-        if stream.device != dev:
-            raise ValueError(f"{name}: tensors on {dev}, stream of {stream.device}")
+        if stream.device.index != dev:
+            raise ValueError(f"{where}: tensors on device {dev}, stream of {stream.device}")
         return torch.cuda.stream(stream)
-    return nullcontext() if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+    return None if torch.cuda.current_device() == dev else torch.cuda.device(dev)
 
 
-def _call(name: str, *args) -> None:
-    _check(getattr(lib(), name)(*args, _torch().cuda.current_stream().cuda_stream), name)
+_RAW_STREAM = None
+
+
+def _raw_stream(dev: int) -> int:
+    """Handle of the current stream of device number `dev`."""
+    global _RAW_STREAM
+    if _RAW_STREAM is None:
+        torch = _torch()
+        # 2.6 us less than by way of a Stream object
+        _RAW_STREAM = getattr(torch._C, "_cuda_getCurrentRawStream",
+                              lambda i: torch.cuda.current_stream(i).cuda_stream)
+    return _RAW_STREAM(dev)
 
 
 def add_rmsnorm(x, weight=None, *, residual=None, residual_out=None, eps: float = 1e-6, y: bool = True,
@@ -714,34 +729,46 @@ def add_rmsnorm(x, weight=None, *, residual=None, residual_out=None, eps: float 
     and as E4M3 codes with a scale per run of 128 (`fp8`).  `residual_out`
     takes h (it may be `residual`: in place); by default a new tensor.
     Returns (y, residual_out, q, q_scales), None for what was not asked."""
+    dev = x.get_device()
+    scope = _elsewhere(dev, stream, "add_rmsnorm")
+    if scope is not None:
+        with scope:
+            return add_rmsnorm(x, weight, residual=residual, residual_out=residual_out, eps=eps, y=y, fp8=fp8)
     torch = _torch()
-    xp, xs = _rows(x, "x")
-    T, d = x.shape
+    xp, xs = _rows(x, dev, "x")
     xt = _moe_type(x.dtype, "x")
+    shape = x.shape
+    T, d = shape
+    rp = rop = wp = yt = q = sc = yp = qp = sp = None
+    rt = rs = ros = wt = 0
+    bf16, f32 = torch.bfloat16, torch.float32
     if residual is not None:
-        if residual.shape != x.shape:
-            raise ValueError(f"residual has shape {tuple(residual.shape)}, x {tuple(x.shape)}")
-        if residual_out is not None and (residual_out.shape != x.shape or residual_out.dtype != residual.dtype):
-            raise ValueError("residual_out must have the residual's shape and dtype")
+        rp, rs = _rows(residual, dev, "residual")
+        rt = _moe_type(residual.dtype, "residual")
+        if residual.shape != shape:
+            raise ValueError(f"residual has shape {tuple(residual.shape)}, x {tuple(shape)}")
+        if residual_out is None:
+            residual_out = torch.empty_like(residual, memory_format=torch.contiguous_format)
+            rop, ros = residual_out.data_ptr(), d
+        else:
+            if residual_out.shape != shape or residual_out.dtype != residual.dtype:
+                raise ValueError("residual_out must have the residual's shape and dtype")
+            rop, ros = _rows(residual_out, dev, "residual_out")
     elif residual_out is not None:
         raise ValueError("residual_out without residual")
-    wp = None if weight is None else _sized(weight, (d,), weight.dtype, "weight")
-    wt = 0 if weight is None else _moe_type(weight.dtype, "weight")
-    with _scope("add_rmsnorm", stream, x, residual, residual_out, weight):
-        dev = x.device
-        rp = rop = None
-        rt = rs = ros = 0
-        if residual is not None:
-            rp, rs = _rows(residual, "residual")
-            rt = _moe_type(residual.dtype, "residual")
-            if residual_out is None:
-                residual_out = torch.empty((T, d), dtype=residual.dtype, device=dev)
-            rop, ros = _rows(residual_out, "residual_out")
-        yt = torch.empty((T, d), dtype=torch.bfloat16, device=dev) if y else None
-        q = torch.empty((T, d), dtype=torch.float8_e4m3fn, device=dev) if fp8 else None
-        sc = torch.empty((T, _runs(d)), dtype=torch.float32, device=dev) if fp8 else None
-        _call("moe_add_rmsnorm", T, d, xp, xt, xs, rp, rop, rt, rs, ros, wp, wt, eps, yt.data_ptr() if y else None,
-              q.data_ptr() if fp8 else None, sc.data_ptr() if fp8 else None)
+    if weight is not None:
+        wt = _moe_type(weight.dtype, "weight")
+        wp = _addr(weight, (weight.dtype,), (d,), dev, "weight")
+    if y:
+        yt = torch.empty_like(x, dtype=bf16, memory_format=torch.contiguous_format)
+        yp = yt.data_ptr()
+    if fp8:
+        q = torch.empty_like(x, dtype=torch.float8_e4m3fn, memory_format=torch.contiguous_format)
+        sc = x.new_empty((T, _runs(d)), dtype=f32)
+        qp, sp = q.data_ptr(), sc.data_ptr()
+    rc = lib().moe_add_rmsnorm(T, d, xp, xt, xs, rp, rop, rt, rs, ros, wp, wt, eps, yp, qp, sp, _raw_stream(dev))
+    if rc:
+        raise MoeError(rc, "moe_add_rmsnorm")
     return yt, residual_out, q, sc
 
 
@@ -751,22 +778,32 @@ def gemm_fp8(a, a_scales, w, w_scales, *, out=None, out_dtype=None, stream=None)
     128 x 128 block of w (w_scales [ceil(N/128)][ceil(K/128)]).  a's and
     out's rows may lie apart.  out_dtype: torch.bfloat16 (default) or
     torch.float32; `out` brings its own."""
+    dev = a.get_device()
+    scope = _elsewhere(dev, stream, "gemm_fp8")
+    if scope is not None:
+        with scope:
+            return gemm_fp8(a, a_scales, w, w_scales, out=out, out_dtype=out_dtype)
     torch = _torch()
-    if a.dtype not in (torch.float8_e4m3fn, torch.uint8):
+    f32, code = (torch.float32,), (torch.float8_e4m3fn, torch.uint8)
+    if a.dtype not in code:
         raise ValueError(f"a has dtype {a.dtype}, expected torch.float8_e4m3fn or torch.uint8")
-    ap, lda = _rows(a, "a")
+    ap, lda = _rows(a, dev, "a")
     M, K = a.shape
     N = w.shape[0]
-    if out is not None and (tuple(out.shape) != (M, N) or (out_dtype is not None and out.dtype != out_dtype)):
-        raise ValueError(f"out must be {out_dtype or out.dtype} of shape {(M, N)}")
-    asp = _sized(a_scales, (M, _runs(K)), torch.float32, "a_scales")
-    wp = _codes(w, (N, K), "w")
-    wsp = _sized(w_scales, (_runs(N), _runs(K)), torch.float32, "w_scales")
-    with _scope("gemm_fp8", stream, a, a_scales, w, w_scales, out):
-        if out is None:
-            out = torch.empty((M, N), dtype=out_dtype or torch.bfloat16, device=a.device)
-        op, ldo = _rows(out, "out")
-        _call("moe_gemm_fp8", M, N, K, ap, lda, asp, wp, wsp, op, _moe_type(out.dtype, "out"), ldo)
+    S = _runs(K)
+    asp = _addr(a_scales, f32, (M, S), dev, "a_scales")
+    wp = _addr(w, code, (N, K), dev, "w")
+    wsp = _addr(w_scales, f32, (_runs(N), S), dev, "w_scales")
+    if out is None:
+        out = a.new_empty((M, N), dtype=out_dtype or torch.bfloat16)
+        op, ldo = out.data_ptr(), N
+    else:
+        if out.shape != (M, N) or (out_dtype is not None and out.dtype != out_dtype):
+            raise ValueError(f"out must be {out_dtype or out.dtype} of shape {(M, N)}")
+        op, ldo = _rows(out, dev, "out")
+    rc = lib().moe_gemm_fp8(M, N, K, ap, lda, asp, wp, wsp, op, _moe_type(out.dtype, "out"), ldo, _raw_stream(dev))
+    if rc:
+        raise MoeError(rc, "moe_gemm_fp8")
     return out
 
 
@@ -776,24 +813,36 @@ def grouped_gemm_fp8(a, a_scales, w, w_scales, offsets, *, perm=None, k: int = 1
     w[e] ([E][N][K]); row r reads a[r], or a[perm[r] // k] with `perm` (int32,
     one entry per sorted row).  Returns out [rows][N], torch.float32 by
     default (what moe_combine takes)."""
+    dev = a.get_device()
+    scope = _elsewhere(dev, stream, "grouped_gemm_fp8")
+    if scope is not None:
+        with scope:
+            return grouped_gemm_fp8(a, a_scales, w, w_scales, offsets, perm=perm, k=k, out=out, out_dtype=out_dtype)
     torch = _torch()
+    f32, i32, code = (torch.float32,), (torch.int32,), (torch.float8_e4m3fn, torch.uint8)
     a_rows, K = a.shape
-    E, N = w.shape[:2]
-    R = a_rows if perm is None else perm.numel()
-    ap = _codes(a, (a_rows, K), "a")
-    asp = _sized(a_scales, (a_rows, _runs(K)), torch.float32, "a_scales")
-    wp = _codes(w, (E, N, K), "w")
-    wsp = _sized(w_scales, (E, _runs(N), _runs(K)), torch.float32, "w_scales")
-    offp = _sized(offsets, (E + 1,), torch.int32, "offsets")
-    permp = None if perm is None else _sized(perm, (R,), torch.int32, "perm")
-    if out is not None and out_dtype is not None and out.dtype != out_dtype:
-        raise ValueError(f"out must be {out_dtype}")
-    with _scope("grouped_gemm_fp8", stream, a, a_scales, w, w_scales, offsets, perm, out):
-        if out is None:
-            out = torch.empty((R, N), dtype=out_dtype or torch.float32, device=a.device)
-        if R:
-            _call("moe_grouped_gemm_fp8", R, E, N, K, ap, a_rows, asp, wp, wsp, offp, permp, int(k),
-                  _sized(out, (R, N), out.dtype, "out"), _moe_type(out.dtype, "out"))
+    E, N, _ = w.shape
+    S = _runs(K)
+    ap = _addr(a, code, (a_rows, K), dev, "a")
+    asp = _addr(a_scales, f32, (a_rows, S), dev, "a_scales")
+    wp = _addr(w, code, (E, N, K), dev, "w")
+    wsp = _addr(w_scales, f32, (E, _runs(N), S), dev, "w_scales")
+    offp = _addr(offsets, i32, (E + 1,), dev, "offsets")
+    R, permp = a_rows, None
+    if perm is not None:
+        R = perm.numel()
+        permp = _addr(perm, i32, (R,), dev, "perm")
+    if out is None:
+        out = a.new_empty((R, N), dtype=out_dtype or torch.float32)
+        op = out.data_ptr()
+    else:
+        op = _addr(out, (out_dtype or out.dtype,), (R, N), dev, "out")
+    ot = _moe_type(out.dtype, "out")
+    if R == 0:
+        return out
+    rc = lib().moe_grouped_gemm_fp8(R, E, N, K, ap, a_rows, asp, wp, wsp, offp, permp, k, op, ot, _raw_stream(dev))
+    if rc:
+        raise MoeError(rc, "moe_grouped_gemm_fp8")
     return out
 
 
@@ -804,28 +853,46 @@ def expert_gate_up_fp8(a, a_scales, gate, gate_scales, up, up_scales, offsets, p
     scale per run of 128.  Returns (act [T*k][f], act_scales), the `a` of a
     grouped_gemm_fp8 with the down matrices.  ws: a uint8 tensor of
     moe_expert_gate_up_fp8_workspace_bytes, allocated by default."""
+    dev = a.get_device()
+    scope = _elsewhere(dev, stream, "expert_gate_up_fp8")
+    if scope is not None:
+        with scope:
+            return expert_gate_up_fp8(a, a_scales, gate, gate_scales, up, up_scales, offsets, perm, k, act=act,
+                                      act_scales=act_scales, ws=ws)
     torch = _torch()
+    f32, i32, code = (torch.float32,), (torch.int32,), (torch.float8_e4m3fn, torch.uint8)
     T, d = a.shape
-    E, f = gate.shape[:2]
-    R = T * k
-    shape = moe_shape(T, d, E, k, f)
-    ptrs = (_codes(a, (T, d), "a"), _sized(a_scales, (T, _runs(d)), torch.float32, "a_scales"),
-            _codes(gate, (E, f, d), "gate"), _sized(gate_scales, (E, _runs(f), _runs(d)), torch.float32, "gate_scales"),
-            _codes(up, (E, f, d), "up"), _sized(up_scales, (E, _runs(f), _runs(d)), torch.float32, "up_scales"),
-            _sized(offsets, (E + 1,), torch.int32, "offsets"), _sized(perm, (R,), torch.int32, "perm"))
-    with _scope("expert_gate_up_fp8", stream, a, a_scales, gate, gate_scales, up, up_scales, offsets, perm, act,
-                act_scales, ws):
-        dev = a.device
-        if act is None:
-            act = torch.empty((R, f), dtype=torch.float8_e4m3fn, device=dev)
-        if act_scales is None:
-            act_scales = torch.empty((R, _runs(f)), dtype=torch.float32, device=dev)
-        if ws is None:
-            n = int(lib().moe_expert_gate_up_fp8_workspace_bytes(ctypes.byref(shape)))
-            ws = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
-        _call("moe_expert_gate_up_fp8", ctypes.byref(shape), *ptrs, _codes(act, (R, f), "act"),
-              _sized(act_scales, (R, _runs(f)), torch.float32, "act_scales"), _ptr(ws, name="ws", allow_none=True),
-              0 if ws is None else ws.numel() * ws.element_size())
+    E, f, _ = gate.shape
+    R, S, NB = T * k, _runs(d), _runs(f)
+    ap = _addr(a, code, (T, d), dev, "a")
+    asp = _addr(a_scales, f32, (T, S), dev, "a_scales")
+    gp = _addr(gate, code, (E, f, d), dev, "gate")
+    gsp = _addr(gate_scales, f32, (E, NB, S), dev, "gate_scales")
+    upp = _addr(up, code, (E, f, d), dev, "up")
+    usp = _addr(up_scales, f32, (E, NB, S), dev, "up_scales")
+    offp = _addr(offsets, i32, (E + 1,), dev, "offsets")
+    permp = _addr(perm, i32, (R,), dev, "perm")
+    if act is None:
+        act = a.new_empty((R, f), dtype=torch.float8_e4m3fn)
+        actp = act.data_ptr()
+    else:
+        actp = _addr(act, code, (R, f), dev, "act")
+    if act_scales is None:
+        act_scales = a.new_empty((R, NB), dtype=torch.float32)
+        scp = act_scales.data_ptr()
+    else:
+        scp = _addr(act_scales, f32, (R, NB), dev, "act_scales")
+    L = lib()
+    shape = ctypes.byref(moe_shape(T, d, E, k, f))
+    if ws is None:
+        n = L.moe_expert_gate_up_fp8_workspace_bytes(shape)
+        ws = a.new_empty(n, dtype=torch.uint8) if n else None
+    wsp, n = (None, 0) if ws is None else (_ptr(ws, name="ws"), ws.numel() * ws.element_size())
+    if ws is not None and ws.get_device() != dev:
+        raise ValueError(f"ws is on {ws.device}, not on device {dev}")
+    rc = L.moe_expert_gate_up_fp8(shape, ap, asp, gp, gsp, upp, usp, offp, permp, actp, scp, wsp, n, _raw_stream(dev))
+    if rc:
+        raise MoeError(rc, "moe_expert_gate_up_fp8")
     return act, act_scales
 
 
@@ -848,15 +915,15 @@ class ExpertsFp8:
     def f(self) -> int:
         return int(self.gate.shape[1])
 
-    def c(self, d: int) -> moe_fp8_experts:
+    def c(self, d: int, dev) -> moe_fp8_experts:
         torch = _torch()
         E, f = self.E, self.f
-        out = moe_fp8_experts()
+        code, f32 = (torch.float8_e4m3fn, torch.uint8), (torch.float32,)
+        p = []
         for name, n, K in (("gate", f, d), ("up", f, d), ("down", d, f)):
-            setattr(out, name, _codes(getattr(self, name), (E, n, K), name))
-            setattr(out, name + "_scales", _sized(getattr(self, name + "_scales"), (E, _runs(n), _runs(K)),
-                                                  torch.float32, name + "_scales"))
-        return out
+            p.append(_addr(getattr(self, name), code, (E, n, K), dev, name))
+            p.append(_addr(getattr(self, name + "_scales"), f32, (E, _runs(n), _runs(K)), dev, name + "_scales"))
+        return moe_fp8_experts(*p)
 
 
 def alloc_workspace_fp8(shape: Shape, device="cuda", stream=None):
@@ -866,7 +933,9 @@ def alloc_workspace_fp8(shape: Shape, device="cuda", stream=None):
     if n == 0:
         raise MoeError(MOE_ERR_SHAPE, "alloc_workspace_fp8")
     ws = torch.empty(n, dtype=torch.uint8, device=device)
-    moe_workspace_init(ws, stream)
+    scope = _elsewhere(ws.get_device(), stream, "alloc_workspace_fp8")
+    with scope or nullcontext():
+        moe_workspace_init(ws)
     return ws
 
 
@@ -875,31 +944,39 @@ def layer_fp8(x, xq, xq_scales, experts: ExpertsFp8, k: int, *, w_router=None, b
     """moe_layer_fp8: the layer with FP8 experts on the outputs of one
     add_rmsnorm (x bf16 for the router, xq and xq_scales for the experts);
     returns (out, topk_ids, topk_w, logits)."""
+    dev = xq.get_device()
+    scope = _elsewhere(dev, stream, "layer_fp8")
+    if scope is not None:
+        with scope:
+            return layer_fp8(x, xq, xq_scales, experts, k, w_router=w_router, bias=bias, logits=logits, ws=ws,
+                             check=check)
     torch = _torch()
+    f32 = (torch.float32,)
     T, d = xq.shape
     E = experts.E
     shape = Shape(T, d, E, k, experts.f)
-    xp = None if x is None else _sized(x, (T, d), torch.bfloat16, "x")
-    xqp = _codes(xq, (T, d), "xq")
-    xsp = _sized(xq_scales, (T, _runs(d)), torch.float32, "xq_scales")
-    wrp = None if w_router is None else _sized(w_router, (E, d), torch.float32, "w_router")
-    bp = None if bias is None else _sized(bias, (E,), torch.float32, "bias")
-    ex, cs = experts.c(d), shape.c()
-    with _scope("layer_fp8", stream, xq, x, xq_scales, w_router, bias, logits, ws,
-                *(getattr(experts, n) for n, _ in moe_fp8_experts._fields_)):
-        dev = xq.device
-        if logits is None:
-            logits = torch.empty((T, E), dtype=torch.float32, device=dev)
-        ids = torch.empty((T, k), dtype=torch.int32, device=dev)
-        w = torch.empty((T, k), dtype=torch.float32, device=dev)
-        out = torch.empty((T, d), dtype=torch.float32, device=dev)
-        if ws is None:
-            ws = alloc_workspace_fp8(shape, dev)
-        _call("moe_layer_fp8", ctypes.byref(cs), xp, xqp, xsp, wrp, bp,
-              _sized(logits, (T, E), torch.float32, "logits"), ctypes.byref(ex), ids.data_ptr(), w.data_ptr(),
-              out.data_ptr(), _ptr(ws, name="ws"), ws.numel() * ws.element_size())
-        if check:
-            check_device_status(ws, "layer_fp8")
+    xp = None if x is None else _addr(x, (torch.bfloat16,), (T, d), dev, "x")
+    xqp = _addr(xq, (torch.float8_e4m3fn, torch.uint8), (T, d), dev, "xq")
+    xsp = _addr(xq_scales, f32, (T, _runs(d)), dev, "xq_scales")
+    wrp = None if w_router is None else _addr(w_router, f32, (E, d), dev, "w_router")
+    bp = None if bias is None else _addr(bias, f32, (E,), dev, "bias")
+    ex, cs = experts.c(d, dev), shape.c()
+    if logits is None:
+        logits = xq.new_empty((T, E), dtype=torch.float32)
+    ids = xq.new_empty((T, k), dtype=torch.int32)
+    w = xq.new_empty((T, k), dtype=torch.float32)
+    out = xq.new_empty((T, d), dtype=torch.float32)
+    if ws is None:
+        ws = alloc_workspace_fp8(shape, xq.device)
+    elif ws.get_device() != dev:
+        raise ValueError(f"ws is on {ws.device}, not on device {dev}")
+    rc = lib().moe_layer_fp8(
+        ctypes.byref(cs), xp, xqp, xsp, wrp, bp, _addr(logits, f32, (T, E), dev, "logits"), ctypes.byref(ex),
+        ids.data_ptr(), w.data_ptr(), out.data_ptr(), _ptr(ws, name="ws"), ws.numel() * ws.element_size(),
+        _raw_stream(dev))
+    _check(rc, "moe_layer_fp8")
+    if check:
+        check_device_status(ws, "layer_fp8")
     return out, ids, w, logits
 
 

@@ -33,8 +33,9 @@ int check_operands(const uint8_t* a, const float* a_scales, const uint8_t* w, co
 }
 
 int run_product(const Fp8Args& a, bool gate_up, hipStream_t st) {
-    if (fp8_blocks(a, gate_up) > 0x7fffffffll) return MOE_ERR_SHAPE;
-    return hip_rc(fp8_uses_skinny(a) ? launch_fp8_skinny(a, gate_up, st) : launch_fp8_tile(a, gate_up, st));
+    const Fp8Plan p = fp8_plan(a, gate_up);
+    if (p.blocks > 0x7fffffffll) return MOE_ERR_SHAPE;
+    return hip_rc(p.path == Fp8Path::kFew ? launch_fp8_few(a, p, gate_up, st) : launch_fp8_tile(a, p, gate_up, st));
 }
 
 Fp8Args grouped_args(int R, int E, int N, int K, const uint8_t* a, int a_rows, const float* a_scales, const uint8_t* w,
@@ -71,18 +72,23 @@ Fp8Args gate_up_args(const moe_shape& s, const uint8_t* a, const float* a_scales
     p.w_scales[1] = up_scales;
     p.act = act;
     p.act_scales = act_scales;
-    if (fp8_uses_skinny(p)) p.hidden = static_cast<float*>(ws);
+    if (fp8_plan(p, true).path != Fp8Path::kMany) {
+        p.hidden = static_cast<float*>(ws);
+        p.flags = reinterpret_cast<unsigned long long*>(static_cast<char*>(ws) + fp8_hidden_bytes(p));
+    }
     return p;
 }
 
-// fp32 silu(g) u of the few-row path.
+// Workspace of a gate/up call: none where a workgroup has whole runs.
 size_t hidden_bytes(const moe_shape& s) {
     static const int32_t grouped = 0;      // stands for offsets: only its presence counts
     Fp8Args p{};
     p.R = s.T * s.k;
     p.E = s.E;
+    p.N = s.f;
+    p.K = s.d;
     p.offsets = &grouped;
-    return p.R && fp8_uses_skinny(p) ? align256(static_cast<size_t>(p.R) * s.f * 4) : 0;
+    return p.R && fp8_plan(p, true).path != Fp8Path::kMany ? fp8_hidden_bytes(p) + fp8_flag_bytes(p) : 0;
 }
 
 struct Fp8LayerCarve {

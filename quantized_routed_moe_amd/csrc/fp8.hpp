@@ -3,6 +3,7 @@
 // interface between the entry points (fp8.hip) and the kernels.
 #pragma once
 
+#include "chain.hpp"
 #include "common.hpp"
 
 namespace qrmoe {
@@ -26,9 +27,11 @@ struct Fp8Args {
     long long out_stride;
     int out_f32;                  // 1: fp32, 0: bf16
     int out_vec;                  // 1: four consecutive values can be stored at once
-    float* hidden;                // gate/up of few rows: silu(g) * u in fp32 [R][N]
-    uint8_t* act;                 // gate/up of many rows: E4M3 [R][N] ...
+    uint8_t* act;                 // gate/up: E4M3 [R][N] ...
     float* act_scales;            // ... and its scales [R][ceil(N/128)]
+    float* hidden;                // gate/up by workgroups of less than 128 columns: silu(g) * u in fp32
+                                  // [R][N] (workspace) ...
+    unsigned long long* flags;    // ... and a flag per workgroup
 };
 
 // Rows [r0, r1) of expert e; e = -1 past the last item.
@@ -88,6 +91,23 @@ __device__ __forceinline__ void zero_rows_past_end(const Fp8Args& a, int n0, int
     }
 }
 
+// Floats that no kernel writes while this one runs, read through the scalar
+// cache: a wave's block scales are one value for all lanes.
+typedef const __attribute__((address_space(4))) float Scalar;
+__device__ __forceinline__ Scalar* scalar_ptr(const float* p) {
+    return reinterpret_cast<Scalar*>(reinterpret_cast<uintptr_t>(p));
+}
+
+// Memory from p on, for copies by a 32-bit lane offset and a scalar offset
+// (raw 32-bit data, no stride; every offset is inside the tensor).
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const uint8_t* p) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p), 0, 0xffffffffu, 4 << 15);
+}
+
+__device__ __forceinline__ void store_hidden(const Fp8Args& a, int r, int n, float v) {
+    __hip_atomic_store(a.hidden + static_cast<size_t>(r) * a.N + n, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
 // Eight E4M3 codes -> bf16, exact (E4M3 has 4 significant bits and an
 // exponent range inside bf16's).
 __device__ __forceinline__ bf16x8 e4m3x8_to_bf16(uint32_t lo, uint32_t hi) {
@@ -108,35 +128,107 @@ __device__ __forceinline__ uint32_t e4m3x4_rne(float a, float b, float c, float 
 
 __device__ __forceinline__ float run_scale(float amax) { return fmaxf(amax / kE4m3Max, kScaleMin); }
 
-// Output columns of one workgroup of the many-row kernel.
-constexpr int fp8_tile_cols(bool gate_up) { return gate_up ? 128 : 256; }
-// Token rows (in 16s) of one workgroup of the many-row kernel.
-inline int fp8_tile_rows16(const Fp8Args& a, bool gate_up) { return 8; }
-
-// Rows an expert has on average when every expert that can have rows has some.
-inline int fp8_mean_rows(const Fp8Args& a) {
-    const int groups = a.offsets ? (a.E < a.R ? a.E : a.R) : 1;
-    return (a.R + groups - 1) / groups;
+// Gate/up by workgroups of COLS < 128 columns: every workgroup has stored its
+// silu(g) u (store_hidden); the one that finishes a run of 128 columns turns
+// it into E4M3.  Each raises its own flag (a value unique to the launch, see
+// chain.hpp, so nothing has to be cleared) once its stores are acknowledged,
+// and reads the flags of the run's workgroups once that store is acknowledged
+// too: whichever flag is acknowledged last, its workgroup sees them all.  When
+// several do, they store the same bytes.  Nobody waits for another.
+template <int COLS>
+__device__ __forceinline__ void finish_run(const Fp8Args& a, const RowItem& it, int item, int n_tile, int n_tiles, int* lds) {
+    constexpr int kPer = kRun / COLS;               // workgroups of a run
+    const unsigned long long tag = chain_tag();
+    unsigned long long* flags = a.flags + static_cast<size_t>(item) * n_tiles;
+    raise_flag(flags + n_tile, tag);
+    const int run = n_tile / kPer, lane = threadIdx.x & 63;
+    if (threadIdx.x < kWave) {
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        const int other = run * kPer + lane;
+        const bool there = lane >= kPer || other >= n_tiles ||
+                           __hip_atomic_load(flags + other, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == tag;
+        const bool all = __all(there);
+        if (lane == 0) *lds = all;
+    }
+    __syncthreads();
+    if (!*lds) return;
+    const int NB = (a.N + kRun - 1) / kRun, n = run * kRun + 2 * lane;
+    const bool live = n < a.N;                      // N is a multiple of 32
+    for (int r = it.r0 + (threadIdx.x >> 6); r < it.r1; r += blockDim.x >> 6) {
+        float v0 = 0.f, v1 = 0.f;
+        if (live) {
+            const unsigned long long v =
+                __hip_atomic_load(reinterpret_cast<const unsigned long long*>(a.hidden + static_cast<size_t>(r) * a.N + n),
+                                  __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            v0 = __uint_as_float(static_cast<uint32_t>(v));
+            v1 = __uint_as_float(static_cast<uint32_t>(v >> 32));
+        }
+        float m = fmaxf(fabsf(v0), fabsf(v1));
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) m = fmaxf(m, __shfl_xor(m, o));
+        const float s = run_scale(m);
+        if (live)
+            *reinterpret_cast<uint16_t*>(a.act + static_cast<size_t>(r) * a.N + n) =
+                static_cast<uint16_t>(e4m3x4_rne(v0 / s, v1 / s, 0.f, 0.f));
+        if (lane == 0) a.act_scales[static_cast<size_t>(r) * NB + run] = s;
+    }
 }
 
-// Token rows (in 16s) of one workgroup of the few-row kernel.
-inline int fp8_skinny_rows16(const Fp8Args& a) {
-    const int m = fp8_mean_rows(a);
-    return m <= 16 ? 1 : m <= 32 ? 2 : 4;
+// How a call is cut into workgroups.  `cols` output columns x `rows` token
+// rows of one expert each.
+enum class Fp8Path {
+    kFew,    // 16 columns x 16 rows, the depth split over 8 waves (fp8_few.hip)
+    kMid,    // 64 columns (gate/up 32) x 64 rows, 4 waves (fp8_tile.hip)
+    kMany    // 256 columns (gate/up 128) x 128 rows, 8 waves (fp8_tile.hip)
+};
+
+struct Fp8Plan {
+    Fp8Path path;
+    int cols, rows, n_tiles;
+    int groups;           // kMid, kMany: groups of column tiles dealt to the XCDs
+    long long blocks;
+};
+
+inline Fp8Plan fp8_plan(const Fp8Args& a, bool gate_up) {
+    Fp8Plan p;
+    // Workgroups of the small tiles, taking it that every expert that can have
+    // rows has some and that half of the experts end in a partial run of rows.
+    // Measured on both sides (us; T tokens, 2 experts each): up to two rounds of
+    // 256 CUs' worth kFew is the fastest (1 x 4096 x 4096: 5.6, kMid 13; 64 rows
+    // 16.4, 16.4; 128 rows 28, 16.4), as for single rows of up to 32 experts
+    // (gate/up, 25 experts: 83, 94).  Beyond, kMid until its workgroups make two
+    // and a half rounds of two per CU (1024 x 4096 x 4096: 41, kMany 41; 512:
+    // 22, 40; 8 experts of 4096 x 2048, T = 256: 30, 36; T = 1024: 71, 62), or
+    // one with both gate and up (8 experts, T = 128: 46, 57; T = 256: 77, 67).
+    const int cols = gate_up ? 128 : 256;
+    const long long experts = a.offsets ? (a.E < a.R ? a.E : a.R) : 1;
+    auto items = [&](int rows) {
+        const long long runs = a.offsets ? a.R / rows + experts / 2 : (static_cast<long long>(a.R) + rows - 1) / rows;
+        return runs > experts ? runs : experts;
+    };
+    const long long few = items(16) * ((a.N + 15) / 16), mid_cols = gate_up ? 32 : 64;
+    const long long mid = items(64) * ((a.N + mid_cols - 1) / mid_cols);
+    p.path = few <= 512 || (a.offsets && a.R <= 32 && a.R <= a.E) ? Fp8Path::kFew
+             : mid <= (gate_up ? 512 : 1280)                     ? Fp8Path::kMid
+                                                                 : Fp8Path::kMany;
+    p.cols = p.path == Fp8Path::kFew ? 16 : p.path == Fp8Path::kMid ? (gate_up ? 32 : 64) : cols;
+    p.rows = p.path == Fp8Path::kFew ? 16 : p.path == Fp8Path::kMid ? 64 : 128;
+    p.n_tiles = (a.N + p.cols - 1) / p.cols;
+    p.groups = p.n_tiles % 4 == 0 ? 4 : p.n_tiles % 2 == 0 ? 2 : 1;
+    const int classes = p.path == Fp8Path::kFew ? 1 : 8 / p.groups;      // of items, one per XCD of a group
+    p.blocks = p.n_tiles * ((row_items(a, p.rows) + classes - 1) / classes * classes);
+    return p;
 }
 
-inline bool fp8_uses_skinny(const Fp8Args& a) { return fp8_mean_rows(a) <= (a.offsets ? 16 : 256); }
-
-// Workgroups of a call's product launch; the entry points refuse more than a
-// grid's 2^31 - 1.
-inline long long fp8_blocks(const Fp8Args& a, bool gate_up) {
-    if (fp8_uses_skinny(a)) return static_cast<long long>((a.N + 15) / 16) * row_items(a, 16 * fp8_skinny_rows16(a));
-    const int cols = fp8_tile_cols(gate_up);
-    return static_cast<long long>((a.N + cols - 1) / cols) * ((row_items(a, 16 * fp8_tile_rows16(a, gate_up)) + 7) / 8 * 8);
+// Workspace of a gate/up call: hidden, then the flags of the most workgroups
+// that the paths with a hidden have.
+inline size_t fp8_hidden_bytes(const Fp8Args& a) { return (static_cast<size_t>(a.R) * a.N * 4 + 255) / 256 * 256; }
+inline size_t fp8_flag_bytes(const Fp8Args& a) {
+    return (static_cast<size_t>((a.N + 15) / 16) * row_items(a, 16) * 8 + 255) / 256 * 256;
 }
 
-hipError_t launch_fp8_skinny(const Fp8Args& a, bool gate_up, hipStream_t st);
-hipError_t launch_fp8_tile(const Fp8Args& a, bool gate_up, hipStream_t st);
+hipError_t launch_fp8_few(const Fp8Args& a, const Fp8Plan& p, bool gate_up, hipStream_t st);
+hipError_t launch_fp8_tile(const Fp8Args& a, const Fp8Plan& p, bool gate_up, hipStream_t st);
 
 struct NormArgs {
     int T, d;

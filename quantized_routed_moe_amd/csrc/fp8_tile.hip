@@ -6,19 +6,21 @@
 // one fp32 multiply-add per output and step adds them, scaled, to the
 // accumulators.
 //
-// A workgroup of eight waves computes 256 weight rows (gate/up: 128 gate rows
-// and the same 128 up rows) x up to 128 token rows of one expert.  Both
-// operands go from memory to LDS as they are, by direct copies of 16 bytes a
-// lane, into a ring of stages of one step each: eight neighbouring lanes take
+// A workgroup computes 256 weight rows (gate/up: 128 gate rows and the same
+// 128 up rows) x up to 128 token rows of one expert with eight waves, or, where
+// that would leave most of the chip idle, 64 (32 and 32) x up to 64 with four.
+// Both operands go from memory to LDS as they are, by direct copies of 16 bytes
+// a lane, into a ring of stages of one step each: eight neighbouring lanes take
 // one row's 128 bytes, whole cache lines.  (Loading the matrix operands
 // straight into registers, lane = row, asks for 16 bytes of another line in
 // every lane; that path stopped at 6 TB/s from the caches, whatever the
 // prefetch distance.)  The 16-byte chunks of a row are stored XOR-swizzled by
 // (row / 2) mod 8, so the 16 rows of a fragment read lie in distinct banks.
 //
-// The waves split the tile by its live rows: 4 x 2 waves of 64 weight rows x
-// 64 token rows above 64 rows, else 8 waves of 32 weight rows x all token
-// rows (64, 32 or 16), whose smaller stages leave room for a deeper ring.
+// The waves of the large tile split it by its live rows: 4 x 2 waves of 64
+// weight rows x 64 token rows above 64 rows, else 8 waves of 32 weight rows x
+// all token rows (64, 32 or 16), whose smaller stages leave room for a deeper
+// ring.
 //
 // FAST: operands stay E4M3 on the 16x16x128 fp8 instruction, whose internal
 // alignment costs about 1.5e-5 relative per step (measured on normal values);
@@ -34,40 +36,31 @@ namespace qrmoe {
 
 namespace {
 
-constexpr int kTileN = 256;
-constexpr int kTileM = 128;
-constexpr int kTileWaves = 8;
-constexpr int kTileThreads = kTileWaves * kWave;
-constexpr int kWBytes = kTileN * kRun;              // weights of a stage
+// A workgroup's tile: TN weight rows x up to TM token rows.
+template <int TN> struct Tile;
+template <> struct Tile<256> {
+    static constexpr int waves = 8, most_rows = 128, lds = 149504;
+};
+template <> struct Tile<64> {
+    static constexpr int waves = 4, most_rows = 64, lds = 67584;
+};
 
 // WM: waves along the token rows, TT: 16-row token tiles of a wave.
-template <int WM, int TT> struct Shape {
+template <int TN, int WM, int TT> struct Shape {
+    static constexpr int waves = Tile<TN>::waves;
     static constexpr int rows = 16 * TT * WM;       // token rows of a stage
-    static constexpr int wn = kTileWaves / WM;      // waves along the weight rows
-    static constexpr int frags = 2 * WM;            // 16-row weight fragments of a wave
-    static constexpr int stage = kWBytes + rows * kRun + 512;     // weights, tokens, token scales
-    static constexpr int ring = rows >= 64 ? 3 : 4;
-    // copies of a wave per stage: weights, tokens (1 KB each), token scales
-    static constexpr int tcopies = rows > 64 ? 2 : 1;
-    static constexpr int loads = 4 + tcopies + 1;
+    static constexpr int wn = waves / WM;           // waves along the weight rows
+    static constexpr int frags = TN / 16 / wn;      // 16-row weight fragments of a wave
+    static constexpr int wbytes = TN * kRun;
+    static constexpr int stage = wbytes + rows * kRun + 512;      // weights, tokens, token scales
+    static constexpr int fit = Tile<TN>::lds / stage;
+    static constexpr int ring = fit > 4 ? 4 : fit;
+    // copies of a wave per stage: weights, tokens (8 rows each), token scales
+    static constexpr int share = rows / waves;      // token rows a wave copies
+    static constexpr int wcopies = TN / waves / 8, tcopies = share > 8 ? share / 8 : 1;
+    static constexpr int loads = wcopies + tcopies + 1;
+    static_assert(ring >= 3 && rows <= Tile<TN>::most_rows, "stage ring");
 };
-constexpr int kTileLds = 149504;
-static_assert(Shape<2, 4>::stage * Shape<2, 4>::ring <= kTileLds && Shape<1, 4>::stage * Shape<1, 4>::ring <= kTileLds &&
-                  Shape<1, 2>::stage * Shape<1, 2>::ring <= kTileLds && Shape<1, 1>::stage * Shape<1, 1>::ring <= kTileLds,
-              "stage ring");
-
-// Memory from p on, for copies by a 32-bit lane offset and a scalar offset
-// (raw 32-bit data, no stride; every offset is inside the tensor).
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const uint8_t* p) {
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p), 0, 0xffffffffu, 4 << 15);
-}
-
-// Floats that no kernel writes while this one runs, read through the scalar
-// cache: a wave's block scales are one value for all lanes.
-typedef const __attribute__((address_space(4))) float Scalar;
-__device__ __forceinline__ Scalar* scalar_ptr(const float* p) {
-    return reinterpret_cast<Scalar*>(reinterpret_cast<uintptr_t>(p));
-}
 
 // At most r (<= R) stages of L copies each are still in flight.
 template <int L, int R>
@@ -129,11 +122,13 @@ __device__ __forceinline__ void step_products(const Operand<false> (&w)[F], cons
 }
 
 // One workgroup's product.  GU: gate/up with SwiGLU and E4M3 output.
-template <int WM, int TT, bool GU, bool FAST>
+template <int TN, int WM, int TT, bool GU, bool FAST>
 __device__ __forceinline__ void tile_body(const Fp8Args& a, const RowItem& it, int n_tile, uint8_t* lds) {
-    using H = Shape<WM, TT>;
-    constexpr int F = H::frags, NST = H::ring, SB = H::stage, L = H::loads;
-    constexpr int kCols = GU ? kTileN / 2 : kTileN;     // output columns
+    using H = Shape<TN, WM, TT>;
+    constexpr int F = H::frags, FG = F / 2, NST = H::ring, SB = H::stage, L = H::loads;
+    constexpr int kCols = GU ? TN / 2 : TN;             // output columns
+    constexpr bool kRuns = GU && kCols == kRun;         // whole runs of 128: E4M3 from here
+    constexpr int kWBytes = H::wbytes;
     constexpr int kMats = GU ? 2 : 1;
 
     const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, col = lane & 15;
@@ -152,21 +147,22 @@ __device__ __forceinline__ void tile_body(const Fp8Args& a, const RowItem& it, i
         return i >= full ? i : s < full ? s : s - full;
     };
 
-    // ---- copies: weight rows 32 wave + 8 i + lane/8 of the tile (gate/up:
-    // waves 0-3 gate, 4-7 up), position lane%8 of the row in LDS holding chunk
+    // ---- copies: the wave's share of the tile's weight rows, 8 rows each
+    // (gate/up: the first half of the waves gate, the second up), position lane%8 of the row in LDS holding chunk
     // (lane%8) ^ (row/2)%8
-    const int mat = GU ? wave >> 2 : 0;
+    constexpr int kShareW = 8 * H::wcopies;             // weight rows of a wave
+    const int mat = GU ? wave / (H::waves / 2) : 0;
     const __amdgpu_buffer_rsrc_t wbuf = buffer_of(a.w[mat] + (static_cast<size_t>(it.e) * a.N + n0) * a.K);
     const int chunk0 = (lane & 7) ^ (lane >> 4);        // rows of even 8 i; of odd 8 i: chunk0 ^ 4
-    int woff[4];
+    int woff[H::wcopies];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int row = (GU ? 32 * (wave & 3) : 32 * wave) + 8 * i + (lane >> 3);
+    for (int i = 0; i < H::wcopies; ++i) {
+        const int row = kShareW * (GU ? wave % (H::waves / 2) : wave) + 8 * i + (lane >> 3);
         woff[i] = min(row, a.N - 1 - n0) * a.K + 16 * (chunk0 ^ (4 * (i & 1)));     // at most 256 * 2^22
     }
     // token rows: the wave's share of the stage's rows, tcopies times 8 (64
     // rows or more) or fewer rows in the low lanes
-    constexpr int kShare = H::rows / kTileWaves;        // rows of a wave: 16, 8, 4 or 2
+    constexpr int kShare = H::share;
     const uint8_t* tsrc[H::tcopies];
 #pragma unroll
     for (int i = 0; i < H::tcopies; ++i) {
@@ -181,10 +177,10 @@ __device__ __forceinline__ void tile_body(const Fp8Args& a, const RowItem& it, i
         // cleared when it is used)
         const int part = s == full ? -1 : 0;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < H::wcopies; ++c) {
             const int k = 16 * (chunk0 ^ (4 * (c & 1)));
             const int back = (full * kRun + k < a.K ? 0 : k) & part;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(wbuf, (lds_void*)(base + (32 * wave + 8 * c) * kRun), 16, woff[c] - back,
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(wbuf, (lds_void*)(base + (kShareW * wave + 8 * c) * kRun), 16, woff[c] - back,
                                                      s * kRun, 0, 0);
         }
 #pragma unroll
@@ -204,8 +200,8 @@ __device__ __forceinline__ void tile_body(const Fp8Args& a, const RowItem& it, i
     Scalar* wscale[kMats];
 #pragma unroll
     for (int f = 0; f < F; ++f) {
-        const int c = GU ? 16 * WM * wn + 16 * (f % WM) : 16 * F * wn + 16 * f;
-        wrow[f] = GU ? 128 * (f / WM) + c : c;
+        const int c = GU ? 16 * FG * wn + 16 * (f % FG) : 16 * F * wn + 16 * f;
+        wrow[f] = GU ? kCols * (f / FG) + c : c;
         wcol[f] = n0 + c;
     }
 #pragma unroll
@@ -256,7 +252,7 @@ __device__ __forceinline__ void tile_body(const Fp8Args& a, const RowItem& it, i
             const float s = ts[16 * t];
 #pragma unroll
             for (int f = 0; f < F; ++f) {
-                const float m = s * w[GU ? f / WM : 0];
+                const float m = s * w[GU ? f / FG : 0];
 #pragma unroll
                 for (int q = 0; q < 4; ++q) acc[f][t][q] = fmaf(p[f][q], m, acc[f][t][q]);
             }
@@ -310,20 +306,32 @@ __device__ __forceinline__ void tile_body(const Fp8Args& a, const RowItem& it, i
                 }
             }
         }
+    } else if constexpr (!kRuns) {
+        // less than a run of columns: through the workspace (finish_run)
+#pragma unroll
+        for (int t = 0; t < TT; ++t) {
+            const int r = it.r0 + 16 * (TT * wm + t) + col;
+#pragma unroll
+            for (int f = 0; f < FG; ++f)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (r < it.r1 && wcol[f] < a.N)
+                        store_hidden(a, r, wcol[f] + 4 * g + i, silu_mul(acc[f][t][i], acc[FG + f][t][i]));
+        }
     } else {
         // v = silu(g) u in place of the gate accumulators; a run's 128
-        // columns are the workgroup's, 4 WM per lane and token
+        // columns are the workgroup's, 4 FG per lane and token
         float* rowmax = reinterpret_cast<float*>(lds);
         __syncthreads();
 #pragma unroll
         for (int t = 0; t < TT; ++t) {
             float m = 0.f;
 #pragma unroll
-            for (int f = 0; f < WM; ++f)
+            for (int f = 0; f < FG; ++f)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     // f is a multiple of 32, so a fragment is inside or outside
-                    acc[f][t][i] = wcol[f] < a.N ? silu_mul(acc[f][t][i], acc[WM + f][t][i]) : 0.f;
+                    acc[f][t][i] = wcol[f] < a.N ? silu_mul(acc[f][t][i], acc[FG + f][t][i]) : 0.f;
                     m = fmaxf(m, fabsf(acc[f][t][i]));
                 }
             m = fmaxf(m, __shfl_xor(m, 16));
@@ -341,7 +349,7 @@ __device__ __forceinline__ void tile_body(const Fp8Args& a, const RowItem& it, i
             const float s = run_scale(m);
             if (wn == 0 && g == 0) a.act_scales[static_cast<size_t>(r) * NB + n_tile] = s;
 #pragma unroll
-            for (int f = 0; f < WM; ++f) {
+            for (int f = 0; f < FG; ++f) {
                 const f32x4 v = acc[f][t];
                 if (wcol[f] < a.N)
                     *reinterpret_cast<uint32_t*>(a.act + static_cast<size_t>(r) * a.N + wcol[f] + 4 * g) =
@@ -351,33 +359,49 @@ __device__ __forceinline__ void tile_body(const Fp8Args& a, const RowItem& it, i
     }
 }
 
-template <bool GU, bool FAST>
-__global__ __launch_bounds__(kTileThreads, 2) void fp8_tile_kernel(Fp8Args a, int n_tiles) {
-    __shared__ __align__(256) uint8_t lds[kTileLds];
-    // workgroup ids go round the 8 XCDs: an XCD takes all column tiles of an item
-    const int xcd = blockIdx.x % 8, at = blockIdx.x / 8;
-    const int n_tile = at % n_tiles, item = at / n_tiles * 8 + xcd;
+template <int TN, bool GU, bool FAST>
+__global__ __launch_bounds__(Tile<TN>::waves* kWave, 2) void fp8_tile_kernel(Fp8Args a, int n_tiles, int groups) {
+    __shared__ __align__(256) uint8_t lds[Tile<TN>::lds];
+    // Workgroup ids go round the 8 XCDs.  An XCD takes one of `groups` groups of
+    // column tiles and every (8 / groups)-th item: its workgroups share both
+    // weight tiles and token rows in its L2.
+    const int xcd = blockIdx.x % 8, at = blockIdx.x / 8, per = n_tiles / groups;
+    const int n_tile = xcd % groups * per + at % per, item = at / per * (8 / groups) + xcd / groups;
     if constexpr (!GU) {
-        const int n0 = n_tile * kTileN;
-        if (a.offsets && item == 0) zero_rows_past_end(a, n0, min(n0 + kTileN, a.N));
+        const int n0 = n_tile * TN;
+        if (a.offsets && item == 0) zero_rows_past_end(a, n0, min(n0 + TN, a.N));
     }
-    const RowItem it = row_item(a, item, kTileM);
+    const RowItem it = row_item(a, item, Tile<TN>::most_rows);
     if (it.e < 0) return;
     const int rows = __builtin_amdgcn_readfirstlane(it.r1 - it.r0);
-    if (rows > 64) tile_body<2, 4, GU, FAST>(a, it, n_tile, lds);
-    else if (rows > 32) tile_body<1, 4, GU, FAST>(a, it, n_tile, lds);
-    else if (rows > 16) tile_body<1, 2, GU, FAST>(a, it, n_tile, lds);
-    else tile_body<1, 1, GU, FAST>(a, it, n_tile, lds);
+    if constexpr (TN == 256) {
+        if (rows > 64) tile_body<TN, 2, 4, GU, FAST>(a, it, n_tile, lds);
+        else if (rows > 32) tile_body<TN, 1, 4, GU, FAST>(a, it, n_tile, lds);
+        else if (rows > 16) tile_body<TN, 1, 2, GU, FAST>(a, it, n_tile, lds);
+        else tile_body<TN, 1, 1, GU, FAST>(a, it, n_tile, lds);
+    } else {
+        if (rows > 32) tile_body<TN, 2, 2, GU, FAST>(a, it, n_tile, lds);
+        else tile_body<TN, 2, 1, GU, FAST>(a, it, n_tile, lds);
+        if constexpr (GU) {
+            __syncthreads();
+            finish_run<TN / 2>(a, it, item, n_tile, n_tiles, reinterpret_cast<int*>(lds));
+        }
+    }
+}
+
+template <int TN>
+void launch(const Fp8Args& a, const Fp8Plan& p, bool gate_up, hipStream_t st) {
+    const int threads = Tile<TN>::waves * kWave, blocks = static_cast<int>(p.blocks);
+    if (gate_up) fp8_tile_kernel<TN, true, false><<<blocks, threads, 0, st>>>(a, p.n_tiles, p.groups);
+    else if (a.out_f32) fp8_tile_kernel<TN, false, false><<<blocks, threads, 0, st>>>(a, p.n_tiles, p.groups);
+    else fp8_tile_kernel<TN, false, true><<<blocks, threads, 0, st>>>(a, p.n_tiles, p.groups);
 }
 
 }  // namespace
 
-hipError_t launch_fp8_tile(const Fp8Args& a, bool gate_up, hipStream_t st) {
-    const int n_tiles = ceil_div(a.N, fp8_tile_cols(gate_up));
-    const int blocks = static_cast<int>(fp8_blocks(a, gate_up));
-    if (gate_up) fp8_tile_kernel<true, false><<<blocks, kTileThreads, 0, st>>>(a, n_tiles);
-    else if (a.out_f32) fp8_tile_kernel<false, false><<<blocks, kTileThreads, 0, st>>>(a, n_tiles);
-    else fp8_tile_kernel<false, true><<<blocks, kTileThreads, 0, st>>>(a, n_tiles);
+hipError_t launch_fp8_tile(const Fp8Args& a, const Fp8Plan& p, bool gate_up, hipStream_t st) {
+    if (p.path == Fp8Path::kMany) launch<256>(a, p, gate_up, st);
+    else launch<64>(a, p, gate_up, st);
     return hipGetLastError();
 }
 

@@ -101,14 +101,18 @@ def test_gate_up_refusals(over, code):
 
 
 def test_workspace_sizes():
+    al = lambda v: (v + 255) // 256 * 256  # noqa: E731
     wb = lambda s: qm.lib().moe_expert_gate_up_fp8_workspace_bytes(ctypes.byref(s))  # noqa: E731
-    assert wb(shape()) == 8 * 128 * 4                     # fp32 silu(g) u of the few-row path
-    assert wb(shape(T=2048, d=4096, E=64, f=2048)) == 0   # the many-row path needs none
+    # fp32 silu(g) u of every row, and an 8-byte flag per 16 columns and run
+    # of 16 rows: at most 8 / 16 + min(E, 8) runs
+    few = al(8 * 128 * 4) + al(8 * 8 * 8)
+    assert wb(shape()) == few
+    assert wb(shape(T=2048, d=4096, E=64, f=2048)) == 0   # workgroups of whole runs need none
     assert wb(shape(k=0)) == 0 and wb(shape(T=0)) == 0
     assert gate_up(s=shape(T=0), ws=None, n=0) == qm.MOE_OK
+    assert gate_up(n=few - 1) == qm.MOE_ERR_WORKSPACE
     lw = lambda s: qm.lib().moe_layer_fp8_workspace_bytes(ctypes.byref(s))  # noqa: E731
-    al = lambda v: (v + 255) // 256 * 256  # noqa: E731
-    assert lw(shape()) == 256 + al(9 * 4) + 2 * al(8 * 4) + al(8 * 128) + al(8 * 4) + 8 * 128 * 4 + al(8 * 256 * 4)
+    assert lw(shape()) == 256 + al(9 * 4) + 2 * al(8 * 4) + al(8 * 128) + al(8 * 4) + few + al(8 * 256 * 4)
     assert lw(shape(f=100)) == 0
 
 
@@ -142,5 +146,5 @@ def test_python_takes_device_tensors_only():
     q, s = torch.zeros((4, 256), dtype=torch.uint8), torch.ones((4, 2))
     for call in (lambda: qm.add_rmsnorm(x), lambda: qm.gemm_fp8(q, s, q, torch.ones((1, 2))),
                  lambda: qm.grouped_gemm_fp8(q, s, q[None], s[None], torch.zeros(2, dtype=torch.int32))):
-        with pytest.raises(ValueError, match="device tensor"):
+        with pytest.raises(ValueError, match="device tensors"):
             call()

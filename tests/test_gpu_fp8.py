@@ -98,7 +98,7 @@ def gemm_case(M, N, K, seed=0):
     return (R8.codes(g, M, K), R8.scales(g, M, runs(K)), R8.codes(g, N, K), R8.scales(g, runs(N), runs(K)))
 
 
-MS = [1, 2, 15, 16, 17, 32, 33, 64, 65, 129, 257, 300, 513]
+MS = [1, 2, 15, 16, 17, 32, 33, 64, 65, 129, 257, 300, 513, 5000]
 
 
 @pytest.mark.parametrize("out_dtype", [BF16, F32])
@@ -245,6 +245,22 @@ def test_gate_up(T, E, k, only, d, f):
         if o[e + 1] > o[e]:
             v, dv = R8.gate_up(a[src[r]], a_s[src[r]], *(m[e] for m in mats))
             R8.check_quantised(q[r], sc[r], v, dv, f"expert {e}")
+
+
+WIDE = [  # T, E, k, only, d, f: workgroups of whole runs, with 1 to 128 and more rows of an expert
+    (200, 16, 4, None, 160, 2080), (40, 64, 1, None, 96, 1152), (90, 8, 1, [3], 288, 6400), (700, 2, 1, None, 128, 5152),
+    (1, 1, 1, None, 4096, 96), (3, 2, 2, None, 2080, 288), (33, 1, 1, None, 3200, 1056), (600, 4, 1, [0, 1], 416, 2048)]
+
+
+@pytest.mark.parametrize("T,E,k,only,d,f", WIDE)
+def test_gate_up_wide(T, E, k, only, d, f):
+    test_gate_up(T, E, k, only, d, f)
+
+
+@pytest.mark.parametrize("out_dtype", [F32, BF16])
+@pytest.mark.parametrize("T,E,k,only,K,N", WIDE)
+def test_grouped_gemm_wide(T, E, k, only, K, N, out_dtype):
+    test_grouped_gemm(T, E, k, only, 2 * N + 1, K, out_dtype)
 
 
 @pytest.mark.parametrize("T", [6, 400])
