@@ -186,6 +186,7 @@ struct Fp8Plan {
     Fp8Path path;
     int cols, rows, n_tiles;
     int groups;           // kMid, kMany: groups of column tiles dealt to the XCDs
+    int items;            // upper bound; the grid may be rounded up beyond it
     long long blocks;
 };
 
@@ -193,13 +194,14 @@ inline Fp8Plan fp8_plan(const Fp8Args& a, bool gate_up) {
     Fp8Plan p;
     // Workgroups of the small tiles, taking it that every expert that can have
     // rows has some and that half of the experts end in a partial run of rows.
-    // Measured on both sides (us; T tokens, 2 experts each): up to two rounds of
-    // 256 CUs' worth kFew is the fastest (1 x 4096 x 4096: 5.6, kMid 13; 64 rows
-    // 16.4, 16.4; 128 rows 28, 16.4), as for single rows of up to 32 experts
-    // (gate/up, 25 experts: 83, 94).  Beyond, kMid until its workgroups make two
-    // and a half rounds of two per CU (1024 x 4096 x 4096: 41, kMany 41; 512:
-    // 22, 40; 8 experts of 4096 x 2048, T = 256: 30, 36; T = 1024: 71, 62), or
-    // one with both gate and up (8 experts, T = 128: 46, 57; T = 256: 77, 67).
+    // Measured on both sides (us; T tokens, two of E experts of 4096 x 2048
+    // each): kFew while a CU gets few of its workgroups (32 x 4096 x 4096: 11.9,
+    // kMid 16.6 in fp32 and 13.4 in bf16; 64 rows 20.7, 21.7 and 16.6; gate/up, E = 8,
+    // T = 32: 29, 29; T = 64: 50, 30) or an expert has a row or two (E = 64,
+    // T = 64: 171, 199, kMany 171).  Then kMid until its workgroups make two
+    // and a half rounds of two per CU (1024 x 4096 x 4096 in bf16: 42, kMany 42;
+    // 512 rows: 23, 40; down, E = 8, T = 256: 33, 36; T = 1024: 68, 56), or one
+    // with both gate and up (E = 8, T = 128: 40, 48; T = 256: 84, 69).
     const int cols = gate_up ? 128 : 256;
     const long long experts = a.offsets ? (a.E < a.R ? a.E : a.R) : 1;
     auto items = [&](int rows) {
@@ -208,15 +210,16 @@ inline Fp8Plan fp8_plan(const Fp8Args& a, bool gate_up) {
     };
     const long long few = items(16) * ((a.N + 15) / 16), mid_cols = gate_up ? 32 : 64;
     const long long mid = items(64) * ((a.N + mid_cols - 1) / mid_cols);
-    p.path = few <= 512 || (a.offsets && a.R <= 32 && a.R <= a.E) ? Fp8Path::kFew
-             : mid <= (gate_up ? 512 : 1280)                     ? Fp8Path::kMid
-                                                                 : Fp8Path::kMany;
+    p.path = few <= (gate_up || a.out_f32 ? 1024 : 768) || (a.offsets && a.R <= 2 * experts) ? Fp8Path::kFew
+             : mid <= (gate_up ? 512 : 1280)                                                ? Fp8Path::kMid
+                                                                                            : Fp8Path::kMany;
     p.cols = p.path == Fp8Path::kFew ? 16 : p.path == Fp8Path::kMid ? (gate_up ? 32 : 64) : cols;
     p.rows = p.path == Fp8Path::kFew ? 16 : p.path == Fp8Path::kMid ? 64 : 128;
     p.n_tiles = (a.N + p.cols - 1) / p.cols;
     p.groups = p.n_tiles % 4 == 0 ? 4 : p.n_tiles % 2 == 0 ? 2 : 1;
     const int classes = p.path == Fp8Path::kFew ? 1 : 8 / p.groups;      // of items, one per XCD of a group
-    p.blocks = p.n_tiles * ((row_items(a, p.rows) + classes - 1) / classes * classes);
+    p.items = static_cast<int>(row_items(a, p.rows));
+    p.blocks = p.n_tiles * ((static_cast<long long>(p.items) + classes - 1) / classes * classes);
     return p;
 }
 

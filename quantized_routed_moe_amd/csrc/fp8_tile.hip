@@ -137,16 +137,6 @@ __device__ __forceinline__ void tile_body(const Fp8Args& a, const RowItem& it, i
     const int n0 = n_tile * kCols;
     const int S = ceil_div(a.K, kRun), NB = ceil_div(a.N, kRun);
     const int full = a.K / kRun;                        // whole steps
-    // Rows of K bytes put the same step of all rows on few memory channels
-    // (256 bytes apart, repeating every 4 KB): the column tiles start their
-    // sums at steps spread over K.  The order depends on the column only.
-    const int rot = full ? static_cast<int>(static_cast<long long>(n_tile) * full / ceil_div(a.N, kCols)) % full : 0;
-    // the i-th step in this column tile's order; the partial step comes last
-    auto nth = [&](int i) {
-        const int s = i + rot;
-        return i >= full ? i : s < full ? s : s - full;
-    };
-
     // ---- copies: the wave's share of the tile's weight rows, 8 rows each
     // (gate/up: the first half of the waves gate, the second up), position lane%8 of the row in LDS holding chunk
     // (lane%8) ^ (row/2)%8
@@ -170,9 +160,8 @@ __device__ __forceinline__ void tile_body(const Fp8Args& a, const RowItem& it, i
         tsrc[i] = a.a + source_row(a, min(it.r0 + row, it.r1 - 1)) * a.a_stride + 16 * ((lane & 7) ^ ((row >> 1) & 7));
     }
     const float* ssrc = a.a_scales + static_cast<size_t>(source_row(a, min(it.r0 + kShare * wave + (lane & 15), it.r1 - 1))) * S;
-    auto issue = [&](int i) {
-        uint8_t* base = lds + (i % NST) * SB;
-        const int s = nth(i);
+    auto issue = [&](int s) {
+        uint8_t* base = lds + (s % NST) * SB;
         // the partial step: a chunk past K is read from the step's start (and
         // cleared when it is used)
         const int part = s == full ? -1 : 0;
@@ -242,7 +231,7 @@ __device__ __forceinline__ void tile_body(const Fp8Args& a, const RowItem& it, i
         Operand<FAST> wo[F];
 #pragma unroll
         for (int f = 0; f < F; ++f) operand(wo[f], lo + wrow[f] * kRun, hi + wrow[f] * kRun);
-        if (!partial) load_ws(nth(min(i + 1, S - 1)));
+        if (!partial) load_ws(min(i + 1, S - 1));
 #pragma unroll
         for (int t = 0; t < TT; ++t) {
             Operand<FAST> to;
@@ -259,7 +248,7 @@ __device__ __forceinline__ void tile_body(const Fp8Args& a, const RowItem& it, i
         }
     };
 
-    load_ws(nth(0));
+    load_ws(0);
     for (int i = 0; i < NST - 1 && i < S; ++i) issue(i);
     // Step i: its copies have arrived (all but the younger stages'), every
     // wave is past step i - 1, whose buffer stage i + NST - 1 then takes.
@@ -360,17 +349,22 @@ __device__ __forceinline__ void tile_body(const Fp8Args& a, const RowItem& it, i
 }
 
 template <int TN, bool GU, bool FAST>
-__global__ __launch_bounds__(Tile<TN>::waves* kWave, 2) void fp8_tile_kernel(Fp8Args a, int n_tiles, int groups) {
+__global__ __launch_bounds__(Tile<TN>::waves* kWave, 2) void fp8_tile_kernel(Fp8Args a, int n_tiles, int groups, int items) {
     __shared__ __align__(256) uint8_t lds[Tile<TN>::lds];
     // Workgroup ids go round the 8 XCDs.  An XCD takes one of `groups` groups of
     // column tiles and every (8 / groups)-th item: its workgroups share both
-    // weight tiles and token rows in its L2.
+    // weight tiles and token rows in its L2.  (One group instead of four, us: 256 x
+    // 4096 x 4096 in fp32 21.7 -> 29.0; 8 experts of 4096 x 2048, T = 256, down
+    // 26.2 -> 32.1, T = 2048 gate/up 183 -> 201; eight groups as four.)
     const int xcd = blockIdx.x % 8, at = blockIdx.x / 8, per = n_tiles / groups;
     const int n_tile = xcd % groups * per + at % per, item = at / per * (8 / groups) + xcd / groups;
     if constexpr (!GU) {
         const int n0 = n_tile * TN;
         if (a.offsets && item == 0) zero_rows_past_end(a, n0, min(n0 + TN, a.N));
     }
+    // offsets that overlap could make an item of the rounded-up grid's rest;
+    // the workspace is sized for `items`
+    if (item >= items) return;
     const RowItem it = row_item(a, item, Tile<TN>::most_rows);
     if (it.e < 0) return;
     const int rows = __builtin_amdgcn_readfirstlane(it.r1 - it.r0);
@@ -392,9 +386,9 @@ __global__ __launch_bounds__(Tile<TN>::waves* kWave, 2) void fp8_tile_kernel(Fp8
 template <int TN>
 void launch(const Fp8Args& a, const Fp8Plan& p, bool gate_up, hipStream_t st) {
     const int threads = Tile<TN>::waves * kWave, blocks = static_cast<int>(p.blocks);
-    if (gate_up) fp8_tile_kernel<TN, true, false><<<blocks, threads, 0, st>>>(a, p.n_tiles, p.groups);
-    else if (a.out_f32) fp8_tile_kernel<TN, false, false><<<blocks, threads, 0, st>>>(a, p.n_tiles, p.groups);
-    else fp8_tile_kernel<TN, false, true><<<blocks, threads, 0, st>>>(a, p.n_tiles, p.groups);
+    if (gate_up) fp8_tile_kernel<TN, true, false><<<blocks, threads, 0, st>>>(a, p.n_tiles, p.groups, p.items);
+    else if (a.out_f32) fp8_tile_kernel<TN, false, false><<<blocks, threads, 0, st>>>(a, p.n_tiles, p.groups, p.items);
+    else fp8_tile_kernel<TN, false, true><<<blocks, threads, 0, st>>>(a, p.n_tiles, p.groups, p.items);
 }
 
 }  // namespace

@@ -1,6 +1,8 @@
 """The FP8 operators on the GPU against float64 (tests/fp8_ref.py), at the
 sizes, strides and routings where a tile, a run or a group can go wrong."""
 
+import ctypes
+
 import pytest
 import torch
 
@@ -261,6 +263,28 @@ def test_gate_up_wide(T, E, k, only, d, f):
 @pytest.mark.parametrize("T,E,k,only,K,N", WIDE)
 def test_grouped_gemm_wide(T, E, k, only, K, N, out_dtype):
     test_grouped_gemm(T, E, k, only, 2 * N + 1, K, out_dtype)
+
+
+@pytest.mark.parametrize("T", [9, 150, 513, 3000])
+def test_gate_up_of_overlapping_offsets_stays_in_its_buffers(T):
+    """Offsets that claim rows many times over make more runs of rows than any
+    sound ones: nothing is written past the workspace or the outputs."""
+    E, k, d, f = 7, 2, 256, 288
+    g = gen(T)
+    R, NB = T * k, 3
+    a, a_s = R8.codes(g, T, d), R8.scales(g, T, 2)
+    gate, up = R8.codes(g, E, f, d), R8.codes(g, E, f, d)
+    gs, us = R8.scales(g, E, NB, 2), R8.scales(g, E, NB, 2)
+    off = torch.tensor([0, R, 0, R, 0, R, 0, R], dtype=torch.int32, device="cuda")
+    perm = torch.arange(R, device="cuda").to(torch.int32)
+    n = qm.lib().moe_expert_gate_up_fp8_workspace_bytes(ctypes.byref(qm.moe_shape(T, d, E, k, f)))
+    guard = 4096
+    ws = torch.full((n + guard,), 0xA5, dtype=torch.uint8, device="cuda")
+    act = torch.full((R * f + guard,), 0xA5, dtype=torch.uint8, device="cuda")
+    sc = torch.full((R * NB + guard,), -3.0, device="cuda")
+    qm.expert_gate_up_fp8(a, a_s, gate, gs, up, us, off, perm, k, act=act[:R * f].view(R, f),
+                          act_scales=sc[:R * NB].view(R, NB), ws=ws[:n] if n else None)
+    assert (ws[n:] == 0xA5).all() and (act[R * f:] == 0xA5).all() and (sc[R * NB:] == -3.0).all()
 
 
 @pytest.mark.parametrize("T", [6, 400])
