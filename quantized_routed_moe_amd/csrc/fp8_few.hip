@@ -11,11 +11,10 @@
 // The weights go from memory to the matrix operand: lane l reads 16-byte
 // chunks l/16 and 4 + l/16 of row l%16's 128 bytes, so the two loads of a step
 // consume 16 whole cache lines.  What keeps enough on its way is the number of
-// waves (45 registers, 32 waves a CU), not requests ahead in each: two chunks
-// of two steps held ahead measured 6.6 us instead of 5.6 at one row x 4096 x
-// 4096 (of which 2.7 are a launch of any size: the weights pass at 5.8 TB/s)
-// and 62 us instead of 48 on 25 experts of 4096 x 2048; copies to LDS, 256
-// bytes of a row by 16 lanes, 6.2 and 55 us.
+// waves (up to 32 a CU), not requests ahead in each: one row x 4096 x 4096 takes
+// 6.0 us (2.7 of them a launch of any size), 25 experts of 4096 x 2048 with a
+// row or two each 40 us, the weights at 5.3 TB/s; with two chunks of two steps
+// held ahead 6.9 and 65 us.
 //
 // Operands are bf16 (E4M3 converts exactly) on the 16x16x32 instruction: the
 // fp8 instructions align their products before adding (1.5e-5 relative per
@@ -29,7 +28,6 @@
 namespace qrmoe {
 
 namespace {
-
 
 __device__ __forceinline__ void to_operands(u32x4 c0, u32x4 c1, bf16x8 (&o)[4]) {
     o[0] = e4m3x8_to_bf16(c0[0], c0[1]);
@@ -128,12 +126,13 @@ __global__ __launch_bounds__(KW* kWave) void fp8_few_kernel(Fp8Args a, int n_til
 
 }  // namespace
 
-// Eight waves where each has three steps or more: at 32 steps eight measured
-// 5.6 us (1 x 4096 x 4096) and four 6.9, at 16 steps (25 experts of 4096 x
-// 2048) eight 48 us and four 43.
+// Eight waves where each has three steps or more (32 steps, 1 x 4096 x 4096:
+// eight 5.9 us, four 7.2; gate/up, 29 experts: 91, 95) or there is no more than
+// one workgroup a CU (16 steps, 1 x 4096 x 2048: 4.3, 4.9); else four (16 steps,
+// 23 experts of 4096 x 2048: 45, 40).
 hipError_t launch_fp8_few(const Fp8Args& a, const Fp8Plan& p, bool gate_up, hipStream_t st) {
     const int blocks = static_cast<int>(p.blocks);
-    const bool eight = ceil_div(a.K, kRun) >= 24;
+    const bool eight = ceil_div(a.K, kRun) >= 24 || blocks <= 256;
     if (gate_up && eight) fp8_few_kernel<2, 8><<<blocks, 8 * kWave, 0, st>>>(a, p.n_tiles);
     else if (gate_up) fp8_few_kernel<2, 4><<<blocks, 4 * kWave, 0, st>>>(a, p.n_tiles);
     else if (eight) fp8_few_kernel<1, 8><<<blocks, 8 * kWave, 0, st>>>(a, p.n_tiles);

@@ -3,11 +3,15 @@
 // type and stored, v = h / sqrt(mean h^2 + eps) * w, y = bf16(v), and per run
 // of 128 values the scale max|v| / 448 with the codes v / scale.
 //
-// Bound by HBM: each input is read and each output written once (T * d * 13
-// bytes for fp32 x, a bf16 stream and both outputs).  One workgroup takes a
-// row and keeps it in registers between the sum of squares and the outputs;
-// a thread holds 8 consecutive values per chunk, so a run of 128 is 16
-// neighbouring lanes and its maximum four lane exchanges.
+// Bound by HBM at many rows: each input is read and each output written once
+// (T * d * 11 bytes for fp32 x, a bf16 stream and both outputs: 2048 x 4096 in
+// 19 us, 4.8 TB/s; a large copy reaches 5.2).  One workgroup takes a row and
+// keeps it in registers between the sum of squares and the outputs; a thread
+// holds 8 consecutive values per chunk, so a run of 128 is 16 neighbouring
+// lanes and its maximum four lane exchanges.  Few rows are bound by the length
+// of a thread's work, mostly the divisions of its codes: the row is spread over
+// as many threads as it has chunks (1 x 4096: 4.1 us, with two chunks a thread
+// 5.3; a launch of any size is 2.7).
 #include "fp8.hpp"
 #include "kernels.hpp"
 
@@ -157,10 +161,16 @@ __global__ __launch_bounds__(THREADS) void norm_kernel(NormArgs a) {
 
 template <bool XF, bool RF, bool WF>
 hipError_t launch(const NormArgs& a, hipStream_t st) {
+    // One chunk a thread up to 4096 (2048 rows: 19.4 us, two 20.3), and up to
+    // 8192 while there is no more than one row a CU (64 rows: one 5.7, two
+    // 6.3; 2048 rows: 39.6, 36.9).  Longer rows are read again: chunks held in
+    // registers took as long (1 x 20000: 9.0, 8.9) or longer (1024 rows: 54,
+    // 50), and 256 threads 17.5 and 59.
     if (a.d <= 2048) norm_kernel<256, 1, XF, RF, WF><<<a.T, 256, 0, st>>>(a);
-    else if (a.d <= 4096) norm_kernel<256, 2, XF, RF, WF><<<a.T, 256, 0, st>>>(a);
-    else if (a.d <= 8192) norm_kernel<256, 4, XF, RF, WF><<<a.T, 256, 0, st>>>(a);
-    else norm_kernel<256, 0, XF, RF, WF><<<a.T, 256, 0, st>>>(a);
+    else if (a.d <= 4096) norm_kernel<512, 1, XF, RF, WF><<<a.T, 512, 0, st>>>(a);
+    else if (a.d <= 8192 && a.T <= 256) norm_kernel<1024, 1, XF, RF, WF><<<a.T, 1024, 0, st>>>(a);
+    else if (a.d <= 8192) norm_kernel<512, 2, XF, RF, WF><<<a.T, 512, 0, st>>>(a);
+    else norm_kernel<1024, 0, XF, RF, WF><<<a.T, 1024, 0, st>>>(a);
     return hipGetLastError();
 }
 

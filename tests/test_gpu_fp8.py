@@ -43,6 +43,12 @@ def test_norm(T, d, xt, rt, wt):
     check_norm(x, res, w, 1e-6, qm.add_rmsnorm(x, w, residual=res, eps=1e-6, fp8=True))
 
 
+@pytest.mark.parametrize("T,d", [(256, 8192), (257, 4128), (300, 8192), (70, 8224)])
+def test_norm_of_many_long_rows(T, d):
+    x, res, w = norm_case(T, d, F32, BF16, BF16, seed=d + T)
+    check_norm(x, res, w, 1e-6, qm.add_rmsnorm(x, w, residual=res, eps=1e-6, fp8=True))
+
+
 def test_norm_outputs_alone():
     x, res, w = norm_case(6, 416, F32, BF16, BF16)
     y, h, q, sc = qm.add_rmsnorm(x, w, residual=res, fp8=True)
