@@ -84,7 +84,8 @@ def norm(x, residual, weight, eps):
     """(h as stored, v, dv): the residual's addition rounded to its type, and
     the norm of what is stored with its relative error counted: the sum of
     squares (8 per chunk of 2048 columns and thread, then 6 + 4 partial sums,
-    squares not rounded apart), half of that through the root, four roundings
+    squares not rounded apart; more threads add at most 12 partial sums and
+    save 8 or more per chunk past the first), half of that through the root, four roundings
     for mean, eps, root and inverse, two products."""
     if residual is not None:
         h = (x.float() + residual.float()).to(residual.dtype)

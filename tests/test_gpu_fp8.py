@@ -381,6 +381,31 @@ def test_chain_captured_and_replayed(T, d, E, k, f):
             assert torch.equal(a, b)
 
 
+def test_two_captured_graphs_share_a_workspace():
+    cases = [layer_case(T, 256, 8, 2, 256, seed=T) for T in (9, 300)]
+    shapes = [qm.Shape(T=c[0].shape[0], d=256, E=8, k=2, f=256) for c in cases]
+    ws = max((qm.alloc_workspace_fp8(s) for s in shapes), key=lambda t: t.numel())
+    want = [[t.clone() for t in run_chain(*c, 2, None)] for c in cases]
+    graphs, got = [], []
+    for c in cases:
+        run_chain(*c, 2, ws)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got.append(run_chain(*c, 2, ws))
+        graphs.append(graph)
+    for order in ((0, 1), (1, 0), (0, 0, 1, 1)):
+        for ts in got:
+            for t in ts:
+                t.zero_()
+        for i in order:
+            graphs[i].replay()
+        torch.cuda.synchronize()
+        for g_, w_ in zip(got, want):
+            for p, q in zip(g_, w_):
+                assert torch.equal(p, q)
+
+
 def test_two_streams_at_once():
     a, b = layer_case(300, 256, 8, 2, 256, seed=1), layer_case(7, 256, 8, 2, 256, seed=2)
     want = [run_chain(*c, 2, None) for c in (a, b)]
@@ -392,6 +417,54 @@ def test_two_streams_at_once():
         for g_, w_ in zip(got, want):
             for p, q in zip(g_, w_):
                 assert torch.equal(p, q)
+
+
+# ------------------------------------------------- offsets beyond 32 bits
+
+@pytest.mark.parametrize("R", [3, 300, 5000])
+def test_grouped_weights_beyond_4_gib(R):
+    E, N, K = 33, 8192, 16384
+    g = gen(R)
+    w = torch.zeros((E, N, K), dtype=torch.uint8, device="cuda")
+    w[-1] = R8.codes(g, N, K).view(torch.uint8)
+    w_s = torch.zeros((E, N // 128, K // 128), device="cuda")
+    w_s[-1] = R8.scales(g, N // 128, K // 128)
+    a, a_s = R8.codes(g, R, K), R8.scales(g, R, K // 128)
+    off = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    off[-1] = R
+    out = qm.grouped_gemm_fp8(a, a_s, w, w_s, off)
+    assert torch.equal(out, qm.grouped_gemm_fp8(a, a_s, w[-1:], w_s[-1:], off[-2:]))
+    want, bound = R8.product(a[-3:], a_s[-3:], w[-1].view(torch.float8_e4m3fn), w_s[-1])
+    R8.check_rounded(out[-3:], want, bound, F32)
+    act, act_s = qm.expert_gate_up_fp8(a, a_s, w, w_s, w, w_s, off, torch.arange(R, device="cuda").to(torch.int32), 1)
+    one = qm.expert_gate_up_fp8(a, a_s, w[-1:], w_s[-1:], w[-1:], w_s[-1:], off[-2:],
+                                torch.arange(R, device="cuda").to(torch.int32), 1)
+    assert torch.equal(act.view(torch.uint8), one[0].view(torch.uint8)) and torch.equal(act_s, one[1])
+
+
+@pytest.mark.parametrize("M", [20, 600])
+def test_gemm_rows_and_outputs_beyond_32_bits(M):
+    N, K = 160, 256
+    a, a_s, w, w_s = gemm_case(M, N, K)
+    step = (5 << 30) // M // 64 * 64
+    rows = torch.zeros(M * step, dtype=torch.uint8, device="cuda").as_strided((M, K), (step, 1))
+    rows.copy_(a.view(torch.uint8))
+    for dt in (F32, BF16):
+        out = torch.zeros(M * step, dtype=dt, device="cuda").as_strided((M, N), (step, 1))
+        qm.gemm_fp8(rows, a_s, w, w_s, out=out)
+        assert torch.equal(out, qm.gemm_fp8(a, a_s, w, w_s, out_dtype=dt))
+
+
+def test_norm_rows_beyond_32_bits():
+    T, d = 40, 4096
+    x, res, w = norm_case(T, d, F32, BF16, BF16)
+    step = (5 << 30) // T // 64 * 64
+    far = lambda t: torch.zeros(T * step, dtype=t.dtype, device="cuda").as_strided((T, d), (step, 1)).copy_(t)  # noqa: E731
+    want = qm.add_rmsnorm(x, w, residual=res, fp8=True)
+    out = far(torch.zeros_like(res))
+    got = qm.add_rmsnorm(far(x), w, residual=far(res), residual_out=out, fp8=True)
+    for p, q in zip(got, want):
+        assert torch.equal(p.contiguous().view(torch.uint8), q.view(torch.uint8))
 
 
 def test_python_refusals():
