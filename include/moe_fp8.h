@@ -90,10 +90,8 @@ int moe_add_rmsnorm(int32_t T, int32_t d, const void* x, int32_t x_type, int64_t
 /* Dense product out [M][N] = a [M][K] . w [N][K]^T of the form above.
    a's rows lie a_stride bytes apart (a multiple of 16, >= K); out's lie
    out_stride values apart (>= N) and are MOE_TYPE_BF16 or MOE_TYPE_F32.
-   fp32 results accumulate exact products of the codes (as bf16 operands) in
-   fp32.  bf16 results of large products use the fp8 matrix instructions,
-   which align the products of a step of 128 before adding them: about 1.5e-5
-   relative on normal values, at most 2^-9 of the step's largest product.
+   Results accumulate exact products of the codes (as bf16 operands) in fp32,
+   whatever the size of the call; a bf16 result is that sum rounded once.
    Limits: M >= 0 (0 enqueues nothing), N >= 1, both below 2^30; K a positive
    multiple of 32 up to 2^22.  Errors: MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_ERR_FORMAT,
    MOE_ERR_ALIGN, MOE_ERR_HIP. */

@@ -22,11 +22,11 @@
 // all token rows (64, 32 or 16), whose smaller stages leave room for a deeper
 // ring.
 //
-// FAST: operands stay E4M3 on the 16x16x128 fp8 instruction, whose internal
-// alignment costs about 1.5e-5 relative per step (measured on normal values);
-// used for bf16 results only.  Otherwise fragments are converted to bf16
-// (exact) and the products run on the 16x16x32 bf16 instruction at half the
-// rate, with fp32 accuracy.
+// Fragments are converted to bf16 (exact) for the 16x16x32 bf16 instruction.
+// The fp8 instructions would take the codes as they are at twice the rate
+// (16x16x128), but they cut a step's products off 16 bits below its largest,
+// which is not a sum in fp32 where large products cancel: 2048 x 4096 x 4096
+// with a bf16 result takes 72 us this way and took 47 that way.
 #include <type_traits>
 
 #include "fp8.hpp"
@@ -83,18 +83,7 @@ __device__ __forceinline__ void stage_barrier() {
 
 // A fragment's operand: chunks l/16 and 4 + l/16 of row l%16 (K is permuted
 // inside the step by that choice, the same for weights and tokens).
-template <bool FAST> struct Operand;
-template <> struct Operand<true> {
-    i32x8 v;
-    __device__ __forceinline__ void set(u32x4 lo, u32x4 hi) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[i] = static_cast<int>(lo[i]);
-            v[4 + i] = static_cast<int>(hi[i]);
-        }
-    }
-};
-template <> struct Operand<false> {
+struct Operand {
     bf16x8 v[4];
     __device__ __forceinline__ void set(u32x4 lo, u32x4 hi) {
         v[0] = e4m3x8_to_bf16(lo[0], lo[1]);
@@ -106,13 +95,7 @@ template <> struct Operand<false> {
 
 // The step's products of a wave's weight fragments and one token tile.
 template <int F>
-__device__ __forceinline__ void step_products(const Operand<true> (&w)[F], const Operand<true>& t, f32x4 (&p)[F]) {
-#pragma unroll
-    for (int f = 0; f < F; ++f)
-        p[f] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w[f].v, t.v, f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
-}
-template <int F>
-__device__ __forceinline__ void step_products(const Operand<false> (&w)[F], const Operand<false>& t, f32x4 (&p)[F]) {
+__device__ __forceinline__ void step_products(const Operand (&w)[F], const Operand& t, f32x4 (&p)[F]) {
 #pragma unroll
     for (int f = 0; f < F; ++f) p[f] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -121,8 +104,9 @@ __device__ __forceinline__ void step_products(const Operand<false> (&w)[F], cons
         for (int f = 0; f < F; ++f) p[f] = mfma16x16x32(w[f].v[j], t.v[j], p[f]);
 }
 
-// One workgroup's product.  GU: gate/up with SwiGLU and E4M3 output.
-template <int TN, int WM, int TT, bool GU, bool FAST>
+// One workgroup's product.  GU: gate/up with SwiGLU and E4M3 output; else
+// BF: bf16 output, not fp32.
+template <int TN, int WM, int TT, bool GU, bool BF>
 __device__ __forceinline__ void tile_body(const Fp8Args& a, const RowItem& it, int n_tile, uint8_t* lds) {
     using H = Shape<TN, WM, TT>;
     constexpr int F = H::frags, FG = F / 2, NST = H::ring, SB = H::stage, L = H::loads;
@@ -217,7 +201,7 @@ __device__ __forceinline__ void tile_body(const Fp8Args& a, const RowItem& it, i
         const uint8_t* tlo = lo + kWBytes + 16 * TT * wm * kRun;
         const uint8_t* thi = hi + kWBytes + 16 * TT * wm * kRun;
         const float* ts = reinterpret_cast<const float*>(base + kWBytes + H::rows * kRun) + 16 * TT * wm + col;
-        auto operand = [&](Operand<FAST>& o, const uint8_t* l, const uint8_t* h) {
+        auto operand = [&](Operand& o, const uint8_t* l, const uint8_t* h) {
             u32x4 c0 = *reinterpret_cast<const u32x4*>(l), c1 = *reinterpret_cast<const u32x4*>(h);
             if constexpr (partial) {
                 if (full * kRun + 16 * g >= a.K) c0 = u32x4{0u, 0u, 0u, 0u};
@@ -228,13 +212,13 @@ __device__ __forceinline__ void tile_body(const Fp8Args& a, const RowItem& it, i
         float w[kMats];
 #pragma unroll
         for (int m = 0; m < kMats; ++m) w[m] = ws[m];
-        Operand<FAST> wo[F];
+        Operand wo[F];
 #pragma unroll
         for (int f = 0; f < F; ++f) operand(wo[f], lo + wrow[f] * kRun, hi + wrow[f] * kRun);
         if (!partial) load_ws(min(i + 1, S - 1));
 #pragma unroll
         for (int t = 0; t < TT; ++t) {
-            Operand<FAST> to;
+            Operand to;
             operand(to, tlo + 16 * t * kRun, thi + 16 * t * kRun);
             f32x4 p[F];
             step_products(wo, to, p);
@@ -280,7 +264,7 @@ __device__ __forceinline__ void tile_body(const Fp8Args& a, const RowItem& it, i
                 const long long at = r * a.out_stride + n;
                 const f32x4 v = acc[f][t];
                 if (a.out_vec && n + 4 <= a.N) {
-                    if constexpr (FAST)
+                    if constexpr (BF)
                         *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.out) + at) =
                             u32x2{f32_to_bf16_rne(v[0]) | static_cast<uint32_t>(f32_to_bf16_rne(v[1])) << 16,
                                   f32_to_bf16_rne(v[2]) | static_cast<uint32_t>(f32_to_bf16_rne(v[3])) << 16};
@@ -289,7 +273,7 @@ __device__ __forceinline__ void tile_body(const Fp8Args& a, const RowItem& it, i
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         if (n + i < a.N) {
-                            if constexpr (FAST) static_cast<uint16_t*>(a.out)[at + i] = f32_to_bf16_rne(v[i]);
+                            if constexpr (BF) static_cast<uint16_t*>(a.out)[at + i] = f32_to_bf16_rne(v[i]);
                             else static_cast<float*>(a.out)[at + i] = v[i];
                         }
                 }
@@ -348,7 +332,7 @@ __device__ __forceinline__ void tile_body(const Fp8Args& a, const RowItem& it, i
     }
 }
 
-template <int TN, bool GU, bool FAST>
+template <int TN, bool GU, bool BF>
 __global__ __launch_bounds__(Tile<TN>::waves* kWave, 2) void fp8_tile_kernel(Fp8Args a, int n_tiles, int groups, int items) {
     __shared__ __align__(256) uint8_t lds[Tile<TN>::lds];
     // Workgroup ids go round the 8 XCDs.  An XCD takes one of `groups` groups of
@@ -369,13 +353,13 @@ __global__ __launch_bounds__(Tile<TN>::waves* kWave, 2) void fp8_tile_kernel(Fp8
     if (it.e < 0) return;
     const int rows = __builtin_amdgcn_readfirstlane(it.r1 - it.r0);
     if constexpr (TN == 256) {
-        if (rows > 64) tile_body<TN, 2, 4, GU, FAST>(a, it, n_tile, lds);
-        else if (rows > 32) tile_body<TN, 1, 4, GU, FAST>(a, it, n_tile, lds);
-        else if (rows > 16) tile_body<TN, 1, 2, GU, FAST>(a, it, n_tile, lds);
-        else tile_body<TN, 1, 1, GU, FAST>(a, it, n_tile, lds);
+        if (rows > 64) tile_body<TN, 2, 4, GU, BF>(a, it, n_tile, lds);
+        else if (rows > 32) tile_body<TN, 1, 4, GU, BF>(a, it, n_tile, lds);
+        else if (rows > 16) tile_body<TN, 1, 2, GU, BF>(a, it, n_tile, lds);
+        else tile_body<TN, 1, 1, GU, BF>(a, it, n_tile, lds);
     } else {
-        if (rows > 32) tile_body<TN, 2, 2, GU, FAST>(a, it, n_tile, lds);
-        else tile_body<TN, 2, 1, GU, FAST>(a, it, n_tile, lds);
+        if (rows > 32) tile_body<TN, 2, 2, GU, BF>(a, it, n_tile, lds);
+        else tile_body<TN, 2, 1, GU, BF>(a, it, n_tile, lds);
         if constexpr (GU) {
             __syncthreads();
             finish_run<TN / 2>(a, it, item, n_tile, n_tiles, reinterpret_cast<int*>(lds));

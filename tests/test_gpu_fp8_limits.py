@@ -1,0 +1,56 @@
+"""The FP8 operators on the GPU where their documentation allows a call that
+sums, sizes or buffers of the ordinary tests do not reach."""
+
+import pytest
+import torch
+
+import fp8_ref as R8
+import quantized_routed_moe_amd as qm
+from fp8_ref import gen, runs
+
+pytestmark = pytest.mark.gpu
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+# ------------------------------------- steps whose large products cancel
+
+def cancelling(g, rows_a, rows_w, K):
+    """Codes whose step of 128 holds two products of +-448^2 that cancel, at
+    places that differ from step to step, and positive products of 0.25 to 4
+    besides: an evaluation that drops what lies 16 bits below the largest
+    product loses all but the large ones."""
+    a = torch.exp2(2 * torch.rand((rows_a, K), generator=g, device="cuda") - 1)
+    w = torch.exp2(2 * torch.rand((rows_w, K), generator=g, device="cuda") - 1)
+    for s in range(runs(K)):
+        i, j = 128 * s + s % 32, 128 * s + 31 - (3 * s) % 16
+        a[:, i], a[:, j], w[:, i], w[:, j] = 448.0, 448.0, 448.0, -448.0
+    return a.to(torch.float8_e4m3fn), w.to(torch.float8_e4m3fn)
+
+
+@pytest.mark.parametrize("out_dtype", [BF16, F32])
+@pytest.mark.parametrize("M,N,K", [(5, 512, 320), (70, 512, 1024), (600, 512, 320), (600, 512, 1024), (5000, 1111, 512)])
+def test_gemm_sums_in_32_bits_where_products_cancel(M, N, K, out_dtype):
+    """Both result types, whatever the number of rows: fp32 sums (their bound,
+    136 roundings of a step's magnitudes, is about 3 here, the sum about 200)
+    and one rounding to the result's type."""
+    g = gen(M + K)
+    a, w = cancelling(g, M, N, K)
+    a_s, w_s = R8.scales(g, M, runs(K)), R8.scales(g, runs(N), runs(K))
+    want, bound = R8.product(a, a_s, w, w_s)
+    R8.check_rounded(qm.gemm_fp8(a, a_s, w, w_s, out_dtype=out_dtype), want, bound, out_dtype)
+
+
+@pytest.mark.parametrize("R", [40, 2400, 9000])
+def test_grouped_bf16_sums_in_32_bits_where_products_cancel(R):
+    g = gen(R)
+    E, N, K = 4, 600, 384
+    mats = [cancelling(g, R if e == 0 else 1, N, K) for e in range(E)]
+    a, w = mats[0][0], torch.stack([m[1] for m in mats])
+    a_s, w_s = R8.scales(g, R, runs(K)), R8.scales(g, E, runs(N), runs(K))
+    off = [0, R // 3, R // 3, R // 2, R]
+    out = qm.grouped_gemm_fp8(a, a_s, w, w_s, torch.tensor(off, dtype=torch.int32, device="cuda"), out_dtype=BF16)
+    for e in range(E):
+        r = slice(off[e], off[e + 1])
+        if off[e + 1] > off[e]:
+            want, bound = R8.product(a[r], a_s[r], w[e], w_s[e])
+            R8.check_rounded(out[r], want, bound, BF16, f"expert {e}")
