@@ -943,7 +943,10 @@ def layer_fp8(x, xq, xq_scales, experts: ExpertsFp8, k: int, *, w_router=None, b
               stream=None, check: bool = False):
     """moe_layer_fp8: the layer with FP8 experts on the outputs of one
     add_rmsnorm (x bf16 for the router, xq and xq_scales for the experts);
-    returns (out, topk_ids, topk_w, logits)."""
+    without w_router, `logits` [T][E] is what it routes on and x may be None.
+    Returns (out, topk_ids, topk_w, logits)."""
+    if w_router is None and logits is None:
+        raise ValueError("layer_fp8 needs w_router or logits")
     dev = xq.get_device()
     scope = _elsewhere(dev, stream, "layer_fp8")
     if scope is not None:

@@ -54,3 +54,43 @@ def test_grouped_bf16_sums_in_32_bits_where_products_cancel(R):
         if off[e + 1] > off[e]:
             want, bound = R8.product(a[r], a_s[r], w[e], w_s[e])
             R8.check_rounded(out[r], want, bound, BF16, f"expert {e}")
+
+
+# ----------------------------------------------------- the layer's routing
+
+def layer_case(T, d, E, k, f, seed=0):
+    g = gen(seed)
+    q, sc = R8.codes(g, T, d), R8.scales(g, T, runs(d), mean=2.0 ** -8)
+    ex = qm.ExpertsFp8(R8.codes(g, E, f, d), R8.scales(g, E, runs(f), runs(d), mean=1 / (112 * d ** 0.5)),
+                       R8.codes(g, E, f, d), R8.scales(g, E, runs(f), runs(d), mean=1 / (112 * d ** 0.5)),
+                       R8.codes(g, E, d, f), R8.scales(g, E, runs(d), runs(f), mean=1 / (112 * f ** 0.5)))
+    return q, sc, ex, torch.randn((T, E), generator=g, device="cuda")
+
+
+@pytest.mark.parametrize("T,d,E,k,f", [(1, 512, 8, 2, 256), (30, 256, 64, 3, 160), (700, 288, 8, 2, 384)])
+def test_layer_of_given_logits(T, d, E, k, f):
+    """No router weights and no x: the layer routes on the logits it is given,
+    and leaves them as they were."""
+    q, sc, ex, lg = layer_case(T, d, E, k, f, seed=T)
+    given = lg.clone()
+    out, ids, tw, back = qm.layer_fp8(None, q, sc, ex, k, logits=lg, check=True)
+    assert back is lg and torch.equal(lg, given)
+    assert torch.equal(ids.long(), lg.topk(k, dim=1).indices)
+    want_w = torch.softmax(lg.double().topk(k, dim=1).values, 1)
+    assert ((tw.double() - want_w).abs() <= 8 * R8.U32).all()      # exp, sum, division: values up to 1
+    off = torch.empty(E + 1, dtype=torch.int32, device="cuda")
+    perm, inv = (torch.empty(T * k, dtype=torch.int32, device="cuda") for _ in range(2))
+    s = qm.Shape(T, d, E, k, f)
+    qm.moe_dispatch(s, ids, off, perm, inv, qm.alloc_workspace(s))
+    act, acts = qm.expert_gate_up_fp8(q, sc, ex.gate, ex.gate_scales, ex.up, ex.up_scales, off, perm, k)
+    want = torch.empty_like(out)
+    qm.moe_combine(s, qm.grouped_gemm_fp8(act, acts, ex.down, ex.down_scales, off), inv, tw, want)
+    assert torch.equal(out, want)
+
+
+def test_layer_refuses_missing_and_misplaced_logits():
+    q, sc, ex, lg = layer_case(4, 256, 8, 2, 128)
+    for bad in (dict(), dict(logits=lg[:, :7].contiguous()), dict(logits=lg.double()), dict(logits=lg.cpu()),
+                dict(w_router=torch.zeros((8, 256), device="cuda")), dict(logits=lg, bias=lg[0])):
+        with pytest.raises((ValueError, qm.MoeError)):
+            qm.layer_fp8(None, q, sc, ex, 2, **bad)
