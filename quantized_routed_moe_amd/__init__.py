@@ -927,14 +927,18 @@ class ExpertsFp8:
 
 
 def alloc_workspace_fp8(shape: Shape, device="cuda", stream=None):
-    """A workspace tensor of moe_layer_fp8 for `shape` (header cleared)."""
+    """A workspace tensor of moe_layer_fp8 for `shape` (header cleared), of
+    `stream` if given: allocated and cleared there."""
     torch = _torch()
     n = int(lib().moe_layer_fp8_workspace_bytes(ctypes.byref(shape.c())))
     if n == 0:
         raise MoeError(MOE_ERR_SHAPE, "alloc_workspace_fp8")
-    ws = torch.empty(n, dtype=torch.uint8, device=device)
-    scope = _elsewhere(ws.get_device(), stream, "alloc_workspace_fp8")
-    with scope or nullcontext():
+    device = torch.device(device)
+    if device.type != "cuda":
+        raise ValueError("alloc_workspace_fp8 takes a device of type cuda")
+    dev = torch.cuda.current_device() if device.index is None else device.index
+    with _elsewhere(dev, stream, "alloc_workspace_fp8") or nullcontext():
+        ws = torch.empty(n, dtype=torch.uint8, device=torch.device("cuda", dev))
         moe_workspace_init(ws)
     return ws
 

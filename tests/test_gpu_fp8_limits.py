@@ -94,3 +94,27 @@ def test_layer_refuses_missing_and_misplaced_logits():
                 dict(w_router=torch.zeros((8, 256), device="cuda")), dict(logits=lg, bias=lg[0])):
         with pytest.raises((ValueError, qm.MoeError)):
             qm.layer_fp8(None, q, sc, ex, 2, **bad)
+
+
+def test_workspace_belongs_to_its_stream():
+    """A freed workspace of a stream is not handed to an allocation of another
+    stream, in which its last kernels may still be running."""
+    s = qm.Shape(300, 512, 8, 2, 512)
+    side = torch.cuda.Stream()
+    torch.cuda.empty_cache()
+    ws = qm.alloc_workspace_fp8(s, stream=side)
+    side.synchronize()
+    assert (ws[:256] == 0).all()
+    at, n = ws.data_ptr(), ws.numel()
+    del ws
+    other = torch.empty(n, dtype=torch.uint8, device="cuda")
+    assert other.data_ptr() != at
+    with torch.cuda.stream(side):
+        again = torch.empty(n, dtype=torch.uint8, device="cuda")
+    assert again.data_ptr() == at
+    q, sc, ex, lg = layer_case(300, 512, 8, 2, 512)
+    want = qm.layer_fp8(None, q, sc, ex, 2, logits=lg)
+    torch.cuda.synchronize()
+    got = qm.layer_fp8(None, q, sc, ex, 2, logits=lg, ws=qm.alloc_workspace_fp8(s, stream=side), stream=side, check=True)
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
