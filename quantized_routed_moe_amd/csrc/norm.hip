@@ -159,6 +159,32 @@ __global__ __launch_bounds__(THREADS) void norm_kernel(NormArgs a) {
     }
 }
 
+// A grid holds fewer than 2^32 threads: rows beyond that go into further
+// launches, all of the kernel that the whole call's size chooses.
+template <int THREADS, int C, bool XF, bool RF, bool WF>
+hipError_t launch_rows(const NormArgs& a, hipStream_t st) {
+    constexpr long long kMost = (1ll << 31) / THREADS;
+    const long long xb = XF ? 4 : 2, rb = RF ? 4 : 2;
+    for (long long t = 0; t < a.T; t += kMost) {
+        NormArgs b = a;
+        b.T = static_cast<int>(a.T - t < kMost ? a.T - t : kMost);
+        b.x = static_cast<const char*>(a.x) + t * a.x_stride * xb;
+        if (a.res) {
+            b.res = static_cast<const char*>(a.res) + t * a.res_stride * rb;
+            b.res_out = static_cast<char*>(a.res_out) + t * a.res_out_stride * rb;
+        }
+        if (a.y) b.y = a.y + t * a.d;
+        if (a.q) {
+            b.q = a.q + t * a.d;
+            b.q_scales = a.q_scales + t * ceil_div(a.d, kRun);
+        }
+        norm_kernel<THREADS, C, XF, RF, WF><<<b.T, THREADS, 0, st>>>(b);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
 template <bool XF, bool RF, bool WF>
 hipError_t launch(const NormArgs& a, hipStream_t st) {
     // One chunk a thread up to 4096 (2048 rows: 19.4 us, two 20.3), and up to
@@ -166,12 +192,11 @@ hipError_t launch(const NormArgs& a, hipStream_t st) {
     // 6.3; 2048 rows: 39.6, 36.9).  Longer rows are read again: chunks held in
     // registers took as long (1 x 20000: 9.0, 8.9) or longer (1024 rows: 54,
     // 50), and 256 threads 17.5 and 59.
-    if (a.d <= 2048) norm_kernel<256, 1, XF, RF, WF><<<a.T, 256, 0, st>>>(a);
-    else if (a.d <= 4096) norm_kernel<512, 1, XF, RF, WF><<<a.T, 512, 0, st>>>(a);
-    else if (a.d <= 8192 && a.T <= 256) norm_kernel<1024, 1, XF, RF, WF><<<a.T, 1024, 0, st>>>(a);
-    else if (a.d <= 8192) norm_kernel<512, 2, XF, RF, WF><<<a.T, 512, 0, st>>>(a);
-    else norm_kernel<1024, 0, XF, RF, WF><<<a.T, 1024, 0, st>>>(a);
-    return hipGetLastError();
+    if (a.d <= 2048) return launch_rows<256, 1, XF, RF, WF>(a, st);
+    if (a.d <= 4096) return launch_rows<512, 1, XF, RF, WF>(a, st);
+    if (a.d <= 8192 && a.T <= 256) return launch_rows<1024, 1, XF, RF, WF>(a, st);
+    if (a.d <= 8192) return launch_rows<512, 2, XF, RF, WF>(a, st);
+    return launch_rows<1024, 0, XF, RF, WF>(a, st);
 }
 
 template <bool XF, bool RF>

@@ -118,3 +118,38 @@ def test_workspace_belongs_to_its_stream():
     got = qm.layer_fp8(None, q, sc, ex, 2, logits=lg, ws=qm.alloc_workspace_fp8(s, stream=side), stream=side, check=True)
     for a, b in zip(got, want):
         assert torch.equal(a, b)
+
+
+# --------------------------------------------- more rows than one grid holds
+
+@pytest.mark.parametrize("T", [(1 << 23) + 3, (1 << 24) + 5])
+def test_norm_of_more_rows_than_a_grid_holds(T):
+    """Rows of 32: at 256 threads a row, 2^24 of them are as many threads as
+    no grid has.  Every row against float64, in parts."""
+    d = 32
+    g = gen(T)
+    x = torch.randn((T, d), generator=g, device="cuda")
+    res = torch.randn((T, d), generator=g, device="cuda").to(BF16)
+    w = (1 + 0.3 * torch.randn(d, generator=g, device="cuda")).to(BF16)
+    y, h, q, sc = qm.add_rmsnorm(x, w, residual=res, fp8=True)
+    for t in range(0, T, 1 << 21):
+        r = slice(t, t + (1 << 21))
+        want_h, v, dv = R8.norm(x[r], res[r], w, 1e-6)
+        assert torch.equal(h[r], want_h)
+        R8.check_rounded(y[r], v, dv, BF16, f"y from row {t}")
+        R8.check_quantised(q[r], sc[r], v, dv, f"q from row {t}")
+
+
+def test_norm_of_many_rows_in_place_and_from_one_row():
+    """The rows of the second launch: one row of x for all, a residual taken
+    in place with other values between its rows, no E4M3 output."""
+    T, d = (1 << 23) + 9, 32
+    g = gen(5)
+    x = torch.randn((1, d), generator=g, device="cuda")
+    buf = torch.randn((T, d + 8), generator=g, device="cuda").to(BF16)
+    want = (x + buf[:, :d].float()).to(BF16)
+    rest = buf[:, d:].clone()
+    y, h, _, _ = qm.add_rmsnorm(x.expand(T, d), None, residual=buf[:, :d], residual_out=buf[:, :d])
+    assert torch.equal(buf[:, :d], want) and torch.equal(buf[:, d:], rest)
+    _, v, dv = R8.norm(want[-64:], None, None, 1e-6)
+    R8.check_rounded(y[-64:], v, dv, BF16)
