@@ -185,7 +185,7 @@ enum class Fp8Path {
 struct Fp8Plan {
     Fp8Path path;
     int cols, rows, n_tiles;
-    int groups;           // kMid, kMany: groups of column tiles dealt to the XCDs
+    int group_bits;       // kMid, kMany: 2^group_bits groups of column tiles are dealt to the XCDs
     int items;            // upper bound; the grid may be rounded up beyond it
     long long blocks;
 };
@@ -216,10 +216,15 @@ inline Fp8Plan fp8_plan(const Fp8Args& a, bool gate_up) {
     p.cols = p.path == Fp8Path::kFew ? 16 : p.path == Fp8Path::kMid ? (gate_up ? 32 : 64) : cols;
     p.rows = p.path == Fp8Path::kFew ? 16 : p.path == Fp8Path::kMid ? 64 : 128;
     p.n_tiles = (a.N + p.cols - 1) / p.cols;
-    p.groups = p.n_tiles % 4 == 0 ? 4 : p.n_tiles % 2 == 0 ? 2 : 1;
-    const int classes = p.path == Fp8Path::kFew ? 1 : 8 / p.groups;      // of items, one per XCD of a group
     p.items = static_cast<int>(row_items(a, p.rows));
-    p.blocks = p.n_tiles * ((static_cast<long long>(p.items) + classes - 1) / classes * classes);
+    // Four groups of column tiles where they come out even, and as many as it
+    // takes that no XCD is without an item (17 x 128256 x 4096, 501 tiles of one
+    // item: 128 us, with one group, that is on one XCD, 500).
+    p.group_bits = p.n_tiles % 4 == 0 ? 2 : p.n_tiles % 2 == 0 ? 1 : 0;
+    while ((8 >> p.group_bits) > p.items) ++p.group_bits;
+    const int groups = 1 << p.group_bits, classes = 8 / groups, per = (p.n_tiles + groups - 1) / groups;
+    p.blocks = p.path == Fp8Path::kFew ? static_cast<long long>(p.n_tiles) * p.items
+                                       : 8ll * per * ((p.items + classes - 1) / classes);
     return p;
 }
 

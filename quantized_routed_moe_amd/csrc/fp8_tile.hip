@@ -333,15 +333,19 @@ __device__ __forceinline__ void tile_body(const Fp8Args& a, const RowItem& it, i
 }
 
 template <int TN, bool GU, bool BF>
-__global__ __launch_bounds__(Tile<TN>::waves* kWave, 2) void fp8_tile_kernel(Fp8Args a, int n_tiles, int groups, int items) {
+__global__ __launch_bounds__(Tile<TN>::waves* kWave, 2) void fp8_tile_kernel(Fp8Args a, int n_tiles, int group_bits, int items) {
     __shared__ __align__(256) uint8_t lds[Tile<TN>::lds];
-    // Workgroup ids go round the 8 XCDs.  An XCD takes one of `groups` groups of
-    // column tiles and every (8 / groups)-th item: its workgroups share both
-    // weight tiles and token rows in its L2.  (One group instead of four, us: 256 x
+    // Workgroup ids go round the 8 XCDs.  An XCD takes one of 2^group_bits groups
+    // of column tiles (as even as they come, the grid has room for the largest)
+    // and every (8 >> group_bits)-th item: its workgroups share both weight tiles
+    // and token rows in its L2.  (One group instead of four, us: 256 x
     // 4096 x 4096 in fp32 21.7 -> 29.0; 8 experts of 4096 x 2048, T = 256, down
     // 26.2 -> 32.1, T = 2048 gate/up 183 -> 201; eight groups as four.)
-    const int xcd = blockIdx.x % 8, at = blockIdx.x / 8, per = n_tiles / groups;
-    const int n_tile = xcd % groups * per + at % per, item = at / per * (8 / groups) + xcd / groups;
+    const int xcd = blockIdx.x % 8, at = blockIdx.x / 8, groups = 1 << group_bits, group = xcd % groups;
+    const int per = (n_tiles + groups - 1) >> group_bits;
+    const int n_tile = (group * n_tiles >> group_bits) + at % per;      // n_tiles <= 2^24
+    const int item = at / per * (8 >> group_bits) + (xcd >> group_bits);
+    if (n_tile >= (group + 1) * n_tiles >> group_bits) return;
     if constexpr (!GU) {
         const int n0 = n_tile * TN;
         if (a.offsets && item == 0) zero_rows_past_end(a, n0, min(n0 + TN, a.N));
@@ -370,9 +374,9 @@ __global__ __launch_bounds__(Tile<TN>::waves* kWave, 2) void fp8_tile_kernel(Fp8
 template <int TN>
 void launch(const Fp8Args& a, const Fp8Plan& p, bool gate_up, hipStream_t st) {
     const int threads = Tile<TN>::waves * kWave, blocks = static_cast<int>(p.blocks);
-    if (gate_up) fp8_tile_kernel<TN, true, false><<<blocks, threads, 0, st>>>(a, p.n_tiles, p.groups, p.items);
-    else if (a.out_f32) fp8_tile_kernel<TN, false, false><<<blocks, threads, 0, st>>>(a, p.n_tiles, p.groups, p.items);
-    else fp8_tile_kernel<TN, false, true><<<blocks, threads, 0, st>>>(a, p.n_tiles, p.groups, p.items);
+    if (gate_up) fp8_tile_kernel<TN, true, false><<<blocks, threads, 0, st>>>(a, p.n_tiles, p.group_bits, p.items);
+    else if (a.out_f32) fp8_tile_kernel<TN, false, false><<<blocks, threads, 0, st>>>(a, p.n_tiles, p.group_bits, p.items);
+    else fp8_tile_kernel<TN, false, true><<<blocks, threads, 0, st>>>(a, p.n_tiles, p.group_bits, p.items);
 }
 
 }  // namespace

@@ -153,3 +153,49 @@ def test_norm_of_many_rows_in_place_and_from_one_row():
     assert torch.equal(buf[:, :d], want) and torch.equal(buf[:, d:], rest)
     _, v, dv = R8.norm(want[-64:], None, None, 1e-6)
     R8.check_rounded(y[-64:], v, dv, BF16)
+
+
+# ------------------------------------------------- wide products of few rows
+
+def time_of(call, n=10):
+    """Least time of a pass, in us, of n passes in a replayed graph."""
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(n):
+            call()
+    best = float("inf")
+    for _ in range(5):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        graph.replay()
+        b.record()
+        torch.cuda.synchronize()
+        best = min(best, a.elapsed_time(b) * 1e3 / n)
+    return best
+
+
+@pytest.mark.parametrize("out_dtype", [BF16, F32])
+@pytest.mark.parametrize("M", [1, 16, 17, 40, 130, 300, 600, 900])
+@pytest.mark.parametrize("N", [12300, 84731, 84736 + 256])
+def test_gemm_wide(M, N, out_dtype):
+    """Column tiles in numbers that four and eight do not divide, of one to
+    several runs of rows."""
+    K = 160
+    g = gen(M + N)
+    a, a_s, w, w_s = R8.codes(g, M, K), R8.scales(g, M, 2), R8.codes(g, N, K), R8.scales(g, runs(N), 2)
+    want, bound = R8.product(a, a_s, w, w_s)
+    R8.check_rounded(qm.gemm_fp8(a, a_s, w, w_s, out_dtype=out_dtype), want, bound, out_dtype)
+
+
+def test_gemm_of_an_odd_number_of_tiles_uses_the_whole_chip():
+    """501 column tiles take about as long as 504; left to one XCD of eight
+    they took three times as long."""
+    M, K, us = 17, 4096, []
+    g = gen(1)
+    a, a_s = R8.codes(g, M, K), R8.scales(g, M, 32)
+    for N in (501 * 256, 504 * 256):
+        w, w_s = R8.codes(g, N, K), R8.scales(g, 2 * N // 256, 32)
+        us.append(time_of(lambda: qm.gemm_fp8(a, a_s, w, w_s)))
+    assert us[0] < 1.5 * us[1], us
