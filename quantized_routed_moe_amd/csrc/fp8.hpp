@@ -197,11 +197,12 @@ inline Fp8Plan fp8_plan(const Fp8Args& a, bool gate_up) {
     // Measured on both sides (us; T tokens, two of E experts of 4096 x 2048
     // each): kFew while a CU gets few of its workgroups (32 x 4096 x 4096: 11.9,
     // kMid 16.0; 64 rows 20.6, 20.1; gate/up, E = 8, T = 32: 29, 29; T = 64:
-    // 50, 30) or an expert has a row or two (E = 64, T = 64: 171, 199, kMany
-    // 171).  Then kMid until its workgroups make two and a half rounds of two
-    // per CU (1024 x 4096 x 4096: 56, kMany 64; 512 rows: 29, 62; down, E = 8,
-    // T = 256: 32, 35; T = 1024: 65, 55), or one with both gate and up (E = 8,
-    // T = 128: 39, 47; T = 256: 81, 68).
+    // 50, 30), the rows of a dense product are four or fewer (x 65536 x 4096: one
+    // row 48, 59, kMany 66; four 54, 59; eight 65, 59) or an expert has a row or
+    // two (E = 64, T = 64: 171, 199, kMany 171).  Then kMid until its workgroups
+    // make two and a half rounds of two per CU (1024 x 4096 x 4096: 56, kMany 64;
+    // 512 rows: 29, 62; down, E = 8, T = 256: 32, 35; T = 1024: 65, 55), or one
+    // with both gate and up (E = 8, T = 128: 39, 47; T = 256: 81, 68).
     const int cols = gate_up ? 128 : 256;
     const long long experts = a.offsets ? (a.E < a.R ? a.E : a.R) : 1;
     auto items = [&](int rows) {
@@ -210,7 +211,7 @@ inline Fp8Plan fp8_plan(const Fp8Args& a, bool gate_up) {
     };
     const long long few = items(16) * ((a.N + 15) / 16), mid_cols = gate_up ? 32 : 64;
     const long long mid = items(64) * ((a.N + mid_cols - 1) / mid_cols);
-    p.path = few <= 1024 || (a.offsets && a.R <= 2 * experts) ? Fp8Path::kFew
+    p.path = few <= 1024 || a.R <= (a.offsets ? 2 * experts : 4) ? Fp8Path::kFew
              : mid <= (gate_up ? 512 : 1280)                     ? Fp8Path::kMid
                                                                  : Fp8Path::kMany;
     p.cols = p.path == Fp8Path::kFew ? 16 : p.path == Fp8Path::kMid ? (gate_up ? 32 : 64) : cols;

@@ -199,3 +199,15 @@ def test_gemm_of_an_odd_number_of_tiles_uses_the_whole_chip():
         w, w_s = R8.codes(g, N, K), R8.scales(g, 2 * N // 256, 32)
         us.append(time_of(lambda: qm.gemm_fp8(a, a_s, w, w_s)))
     assert us[0] < 1.5 * us[1], us
+
+
+def test_gemm_of_one_row_streams_the_weights():
+    """One row of a wide product costs less than 17 (0.80 of them); on their
+    tile it cost the same."""
+    N, K, us = 65536, 4096, []
+    g = gen(2)
+    w, w_s = R8.codes(g, N, K), R8.scales(g, N // 128, 32)
+    for M in (1, 17):
+        a, a_s = R8.codes(g, M, K), R8.scales(g, M, 32)
+        us.append(time_of(lambda: qm.gemm_fp8(a, a_s, w, w_s)))
+    assert us[0] < 0.92 * us[1], us
