@@ -201,13 +201,15 @@ def test_gemm_of_an_odd_number_of_tiles_uses_the_whole_chip():
     assert us[0] < 1.5 * us[1], us
 
 
-def test_gemm_of_one_row_streams_the_weights():
-    """One row of a wide product costs less than 17 (0.80 of them); on their
-    tile it cost the same."""
-    N, K, us = 65536, 4096, []
+@pytest.mark.parametrize("out_dtype", [BF16, F32])
+@pytest.mark.parametrize("M", [1, 4])
+def test_gemm_of_few_rows_does_not_depend_on_the_columns(M, out_dtype):
+    """Up to four rows: a column's sum is the same bits in a product of 256
+    columns and of 90000, on one kernel whatever the columns."""
+    N, K = 90000, 4096
     g = gen(2)
-    w, w_s = R8.codes(g, N, K), R8.scales(g, N // 128, 32)
-    for M in (1, 17):
-        a, a_s = R8.codes(g, M, K), R8.scales(g, M, 32)
-        us.append(time_of(lambda: qm.gemm_fp8(a, a_s, w, w_s)))
-    assert us[0] < 0.92 * us[1], us
+    a, a_s, w, w_s = R8.codes(g, M, K), R8.scales(g, M, 32), R8.codes(g, N, K), R8.scales(g, runs(N), 32)
+    wide = qm.gemm_fp8(a, a_s, w, w_s, out_dtype=out_dtype)
+    for n in (0, 1 << 14, 1 << 16):
+        few = qm.gemm_fp8(a, a_s, w[n:n + 256], w_s[n // 128:n // 128 + 2], out_dtype=out_dtype)
+        assert torch.equal(wide[:, n:n + 256], few)
