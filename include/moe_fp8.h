@@ -93,7 +93,9 @@ int moe_add_rmsnorm(int32_t T, int32_t d, const void* x, int32_t x_type, int64_t
    Results accumulate exact products of the codes (as bf16 operands) in fp32,
    whatever the size of the call; a bf16 result is that sum rounded once.
    Limits: M >= 0 (0 enqueues nothing), N >= 1, both below 2^30; K a positive
-   multiple of 32 up to 2^22.  Errors: MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_ERR_FORMAT,
+   multiple of 32 up to 2^22; the workgroups, one per tile of 128 rows x 256
+   columns and some that make the rounds over eight XCDs whole, fewer than 2^23
+   (fewer than 2^22 tiles always fit).  Errors: MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_ERR_FORMAT,
    MOE_ERR_ALIGN, MOE_ERR_HIP. */
 int moe_gemm_fp8(int32_t M, int32_t N, int32_t K, const uint8_t* a, int64_t a_stride, const float* a_scales,
                  const uint8_t* w, const float* w_scales, void* out, int32_t out_type, int64_t out_stride,
@@ -111,7 +113,8 @@ int moe_gemm_fp8(int32_t M, int32_t N, int32_t K, const uint8_t* a, int64_t a_st
    Experts without rows are not read.  Offsets outside [0, R] and rows
    src(r) outside [0, a_rows) are clamped into range, never followed.
    Limits: R >= 0 (0 enqueues nothing), 1 <= E <= 64, N and K as
-   moe_gemm_fp8, k >= 1, a_rows >= 1.  Errors as moe_gemm_fp8. */
+   moe_gemm_fp8, k >= 1, a_rows >= 1, workgroups as there with R / 128 +
+   min(E, R) runs of rows.  Errors as moe_gemm_fp8. */
 int moe_grouped_gemm_fp8(int32_t R, int32_t E, int32_t N, int32_t K, const uint8_t* a, int32_t a_rows,
                          const float* a_scales, const uint8_t* w, const float* w_scales, const int32_t* offsets,
                          const int32_t* perm, int32_t k, void* out, int32_t out_type, hipStream_t stream);
@@ -130,7 +133,7 @@ int moe_grouped_gemm_fp8(int32_t R, int32_t E, int32_t N, int32_t K, const uint8
    ws: moe_expert_gate_up_fp8_workspace_bytes(shape) bytes (0: ws may be
    NULL), uninitialised; one call at a time.  Limits as include/moe.h
    (moe_shape) with d <= 2^22 (and f, in moe_layer_fp8), offsets and perm
-   clamped as above.  Errors: as
+   clamped as above, workgroups as there with tiles of 128 columns.  Errors: as
    moe_expert_ffn. */
 size_t moe_expert_gate_up_fp8_workspace_bytes(const moe_shape* shape);
 int moe_expert_gate_up_fp8(const moe_shape* shape, const uint8_t* a, const float* a_scales, const uint8_t* gate,

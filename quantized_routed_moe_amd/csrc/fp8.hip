@@ -34,7 +34,7 @@ int check_operands(const uint8_t* a, const float* a_scales, const uint8_t* w, co
 
 int run_product(const Fp8Args& a, bool gate_up, hipStream_t st) {
     const Fp8Plan p = fp8_plan(a, gate_up);
-    if (p.blocks > 0x7fffffffll) return MOE_ERR_SHAPE;
+    if (p.blocks >= kMostBlocks) return MOE_ERR_SHAPE;
     return hip_rc(p.path == Fp8Path::kFew ? launch_fp8_few(a, p, gate_up, st) : launch_fp8_tile(a, p, gate_up, st));
 }
 
@@ -257,6 +257,7 @@ int moe_layer_fp8(const moe_shape* shape, const uint16_t* x, const uint8_t* xq, 
         if ((rc = hip_rc(launch_dispatch(s, topk_ids, offsets, perm, inv, static_cast<uint32_t*>(ws), stream))) != MOE_OK)
             return rc;
     }
+    // both fit a grid: T*k*f < 2^31 and f <= 2^22, and so for d
     const Fp8Args gu = gate_up_args(s, xq, xq_scales, ex.gate, ex.gate_scales, ex.up, ex.up_scales, offsets, perm, act,
                                     act_scales, base + c.hidden);
     if ((rc = run_product(gu, true, stream)) != MOE_OK) return rc;

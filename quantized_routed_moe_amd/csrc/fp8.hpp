@@ -190,6 +190,9 @@ struct Fp8Plan {
     long long blocks;
 };
 
+// A grid holds fewer than 2^32 threads, and no workgroup here has more than 512.
+constexpr long long kMostBlocks = 1ll << 23;
+
 inline Fp8Plan fp8_plan(const Fp8Args& a, bool gate_up) {
     Fp8Plan p;
     // Workgroups of the small tiles, taking it that every expert that can have
@@ -211,9 +214,10 @@ inline Fp8Plan fp8_plan(const Fp8Args& a, bool gate_up) {
     };
     const long long few = items(16) * ((a.N + 15) / 16), mid_cols = gate_up ? 32 : 64;
     const long long mid = items(64) * ((a.N + mid_cols - 1) / mid_cols);
-    p.path = few <= 1024 || a.R <= (a.offsets ? 2 * experts : 4) ? Fp8Path::kFew
-             : mid <= (gate_up ? 512 : 1280)                     ? Fp8Path::kMid
-                                                                 : Fp8Path::kMany;
+    const long long few_blocks = row_items(a, 16) * ((a.N + 15) / 16);
+    p.path = few <= 1024 || (a.R <= (a.offsets ? 2 * experts : 4) && few_blocks < kMostBlocks) ? Fp8Path::kFew
+             : mid <= (gate_up ? 512 : 1280)                                                 ? Fp8Path::kMid
+                                                                                             : Fp8Path::kMany;
     p.cols = p.path == Fp8Path::kFew ? 16 : p.path == Fp8Path::kMid ? (gate_up ? 32 : 64) : cols;
     p.rows = p.path == Fp8Path::kFew ? 16 : p.path == Fp8Path::kMid ? 64 : 128;
     p.n_tiles = (a.N + p.cols - 1) / p.cols;

@@ -1,5 +1,7 @@
 """Limits and refusals of the FP8 entry points that need no GPU."""
 
+import ctypes
+
 import pytest
 import torch
 
@@ -19,3 +21,25 @@ def test_layer_needs_a_router_or_logits():
 def test_workspace_is_a_device_tensor():
     with pytest.raises(ValueError, match="type cuda"):
         qm.alloc_workspace_fp8(qm.Shape(4, 256, 8, 2, 128), device="cpu")
+
+
+A = 0x10000            # fake, 16-byte aligned "device" address (never dereferenced)
+
+
+# A grid has fewer than 2^32 threads, which is 2^23 workgroups of 512, not the
+# 2^31 of a workgroup's index: refused before any HIP call.
+
+@pytest.mark.parametrize("M,N", [((1 << 30) - 1, 1), (1 << 20, 1 << 20), (129, (1 << 30) - 1), (1 << 29, 257)])
+def test_gemm_of_more_tiles_than_a_grid_holds(M, N):
+    assert qm.lib().moe_gemm_fp8(M, N, 32, A, 32, A, A, A, A, qm.MOE_TYPE_BF16, N, None) == qm.MOE_ERR_SHAPE
+
+
+@pytest.mark.parametrize("R,N", [(128, (1 << 30) - 1), ((1 << 30) - 1, 1 << 12), (3, (1 << 30) - 1), (64, 1 << 25)])
+def test_grouped_gemm_of_more_tiles_than_a_grid_holds(R, N):
+    assert qm.lib().moe_grouped_gemm_fp8(R, 64, N, 32, A, R, A, A, A, A, None, 1, A, qm.MOE_TYPE_F32,
+                                         None) == qm.MOE_ERR_SHAPE
+
+
+def test_gate_up_of_more_tiles_than_a_grid_holds():
+    s = ctypes.byref(qm.moe_shape(64, 32, 64, 2, (1 << 24) - 32))
+    assert qm.lib().moe_expert_gate_up_fp8(s, A, A, A, A, A, A, A, A, A, A, A, 1 << 40, None) == qm.MOE_ERR_SHAPE

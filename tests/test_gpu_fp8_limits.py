@@ -213,3 +213,22 @@ def test_gemm_of_few_rows_does_not_depend_on_the_columns(M, out_dtype):
     for n in (0, 1 << 14, 1 << 16):
         few = qm.gemm_fp8(a, a_s, w[n:n + 256], w_s[n // 128:n // 128 + 2], out_dtype=out_dtype)
         assert torch.equal(wide[:, n:n + 256], few)
+
+
+def test_grouped_gemm_of_more_columns_than_few_row_workgroups_fit():
+    """A row or two an expert of 2^21 columns: more workgroups of 16 columns
+    than a grid holds."""
+    E, N, K, R = 64, (1 << 21) - 48, 32, 100
+    g = gen(7)
+    w = torch.randint(0, 120, (E, N, K), generator=g, device="cuda", dtype=torch.uint8)       # codes of 0 to 256
+    a, a_s, w_s = R8.codes(g, R, K), R8.scales(g, R, 1), R8.scales(g, E, runs(N), 1)
+    off = torch.linspace(0, R, E + 1, device="cuda").to(torch.int32)
+    out = qm.grouped_gemm_fp8(a, a_s, w, w_s, off)
+    o = off.tolist()
+    for e in range(E):
+        r = slice(o[e], o[e + 1])
+        for n in (0, 1 << 20, N - 300):
+            n -= n % 128
+            c = slice(n, min(n + 300, N))
+            want, bound = R8.product(a[r], a_s[r], w[e, c].view(torch.float8_e4m3fn), w_s[e, n // 128:runs(c.stop)])
+            R8.check_rounded(out[r, c], want, bound, F32)
