@@ -114,7 +114,7 @@ int moe_gemm_fp8(int32_t M, int32_t N, int32_t K, const uint8_t* a, int64_t a_st
    src(r) outside [0, a_rows) are clamped into range, never followed.
    Limits: R >= 0 (0 enqueues nothing), 1 <= E <= 64, N and K as
    moe_gemm_fp8, k >= 1, a_rows >= 1, workgroups as there with R / 128 +
-   min(E, R) runs of rows.  Errors as moe_gemm_fp8. */
+   min(E + 1, R) runs of rows.  Errors as moe_gemm_fp8. */
 int moe_grouped_gemm_fp8(int32_t R, int32_t E, int32_t N, int32_t K, const uint8_t* a, int32_t a_rows,
                          const float* a_scales, const uint8_t* w, const float* w_scales, const int32_t* offsets,
                          const int32_t* perm, int32_t k, void* out, int32_t out_type, hipStream_t stream);
@@ -133,7 +133,8 @@ int moe_grouped_gemm_fp8(int32_t R, int32_t E, int32_t N, int32_t K, const uint8
    ws: moe_expert_gate_up_fp8_workspace_bytes(shape) bytes (0: ws may be
    NULL), uninitialised; one call at a time.  Limits as include/moe.h
    (moe_shape) with d <= 2^22 (and f, in moe_layer_fp8), offsets and perm
-   clamped as above, workgroups as there with tiles of 128 columns.  Errors: as
+   clamped as above, workgroups as there with tiles of 128
+   columns and no run past offsets[E].  Errors: as
    moe_expert_ffn. */
 size_t moe_expert_gate_up_fp8_workspace_bytes(const moe_shape* shape);
 int moe_expert_gate_up_fp8(const moe_shape* shape, const uint8_t* a, const float* a_scales, const uint8_t* gate,

@@ -34,16 +34,20 @@ struct Fp8Args {
     unsigned long long* flags;    // ... and a flag per workgroup
 };
 
-// Rows [r0, r1) of expert e; e = -1 past the last item.
+// Rows [r0, r1) of expert e; e = E: rows at or past offsets[E], to be zeroed;
+// e = -1 past the last item.
 struct RowItem {
     int e, r0, r1;
 };
 
 // Item idx of the schedule that cuts every expert's rows into runs of at
-// most `rows`, experts in id order.  Lane e of the calling wave reads expert
-// e's bounds (clamped to [0, R], so no offset is followed out of range) and
-// a wave scan over the experts' item counts finds the owner.  Uniform.
-__device__ __forceinline__ RowItem row_item(const Fp8Args& a, int idx, int rows) {
+// most `rows`, experts in id order, and after them (tail) the rows at or past
+// offsets[E], whose zeros so are spread over the grid as the products are (16384
+// rows x 4096 in fp32, 64 of them live: 41 us; by the workgroups of the first
+// item 1280).  Lane e of the calling wave reads expert e's bounds (clamped to
+// [0, R], so no offset is followed out of range) and a wave scan over the
+// experts' item counts finds the owner.  Uniform.
+__device__ __forceinline__ RowItem row_item(const Fp8Args& a, int idx, int rows, bool tail) {
     if (!a.offsets) {
         const int r0 = idx * rows;
         return RowItem{r0 < a.R ? 0 : -1, r0, min(a.R, r0 + rows)};
@@ -62,16 +66,22 @@ __device__ __forceinline__ RowItem row_item(const Fp8Args& a, int idx, int rows)
         if (lane >= o) incl += v;
     }
     const uint64_t hit = __ballot(idx >= incl - items && idx < incl);
-    if (!hit) return RowItem{-1, 0, 0};
+    if (!hit) {
+        if (!tail) return RowItem{-1, 0, 0};
+        const long long r0 = min(max(a.offsets[a.E], 0), a.R) + static_cast<long long>(idx - lane_value(incl, 63)) * rows;
+        if (r0 >= a.R) return RowItem{-1, 0, 0};
+        return RowItem{a.E, static_cast<int>(r0), static_cast<int>(min(r0 + rows, static_cast<long long>(a.R)))};
+    }
     const int e = __ffsll(static_cast<unsigned long long>(hit)) - 1;
     const int r0 = lane_value(lo, e) + (idx - lane_value(incl - items, e)) * rows;
     return RowItem{e, r0, min(lane_value(hi, e), r0 + rows)};
 }
 
-// Upper bound of the items of any offsets.
-inline long long row_items(const Fp8Args& a, int rows) {
+// Upper bound of the items of any sound offsets.
+inline long long row_items(const Fp8Args& a, int rows, bool tail) {
     if (!a.offsets) return (static_cast<long long>(a.R) + rows - 1) / rows;
-    return a.R / rows + (a.E < a.R ? a.E : a.R);
+    const int groups = a.E + tail;
+    return a.R / rows + (groups < a.R ? groups : a.R);
 }
 
 // Row of `a` that sorted row r reads.
@@ -80,14 +90,22 @@ __device__ __forceinline__ int source_row(const Fp8Args& a, int r) {
     return min(max(s, 0), a.a_rows - 1);
 }
 
-// Rows at or past offsets[E], columns [n0, n1): zeros.
-__device__ __forceinline__ void zero_rows_past_end(const Fp8Args& a, int n0, int n1) {
-    const int first = min(max(a.offsets[a.E], 0), a.R);
-    const int cols = n1 - n0;
-    for (long long i = threadIdx.x; i < static_cast<long long>(a.R - first) * cols; i += blockDim.x) {
-        const long long at = (first + i / cols) * a.out_stride + n0 + i % cols;
-        if (a.out_f32) static_cast<float*>(a.out)[at] = 0.f;
-        else static_cast<uint16_t*>(a.out)[at] = 0;
+// Zeros in the rows of an item and COLS columns from n0 on.
+template <int COLS>
+__device__ __forceinline__ void zero_tile(const Fp8Args& a, const RowItem& it, int n0) {
+    constexpr int kChunks = COLS / 4;
+    for (int i = threadIdx.x; i < (it.r1 - it.r0) * kChunks; i += blockDim.x) {
+        const int n = n0 + 4 * (i % kChunks);
+        const long long at = (it.r0 + i / kChunks) * a.out_stride + n;
+        if (a.out_vec && n + 4 <= a.N) {
+            if (a.out_f32) *reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + at) = f32x4{0.f, 0.f, 0.f, 0.f};
+            else *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.out) + at) = u32x2{0u, 0u};
+        } else {
+            for (int c = 0; c < 4 && n + c < a.N; ++c) {
+                if (a.out_f32) static_cast<float*>(a.out)[at + c] = 0.f;
+                else static_cast<uint16_t*>(a.out)[at + c] = 0;
+            }
+        }
     }
 }
 
@@ -214,14 +232,14 @@ inline Fp8Plan fp8_plan(const Fp8Args& a, bool gate_up) {
     };
     const long long few = items(16) * ((a.N + 15) / 16), mid_cols = gate_up ? 32 : 64;
     const long long mid = items(64) * ((a.N + mid_cols - 1) / mid_cols);
-    const long long few_blocks = row_items(a, 16) * ((a.N + 15) / 16);
+    const long long few_blocks = row_items(a, 16, !gate_up) * ((a.N + 15) / 16);
     p.path = few <= 1024 || (a.R <= (a.offsets ? 2 * experts : 4) && few_blocks < kMostBlocks) ? Fp8Path::kFew
              : mid <= (gate_up ? 512 : 1280)                                                 ? Fp8Path::kMid
                                                                                              : Fp8Path::kMany;
     p.cols = p.path == Fp8Path::kFew ? 16 : p.path == Fp8Path::kMid ? (gate_up ? 32 : 64) : cols;
     p.rows = p.path == Fp8Path::kFew ? 16 : p.path == Fp8Path::kMid ? 64 : 128;
     p.n_tiles = (a.N + p.cols - 1) / p.cols;
-    p.items = static_cast<int>(row_items(a, p.rows));
+    p.items = static_cast<int>(row_items(a, p.rows, !gate_up));
     // Four groups of column tiles where they come out even, and as many as it
     // takes that no XCD is without an item (17 x 128256 x 4096, 501 tiles of one
     // item: 128 us, with one group, that is on one XCD, 500).
@@ -237,7 +255,7 @@ inline Fp8Plan fp8_plan(const Fp8Args& a, bool gate_up) {
 // that the paths with a hidden have.
 inline size_t fp8_hidden_bytes(const Fp8Args& a) { return (static_cast<size_t>(a.R) * a.N * 4 + 255) / 256 * 256; }
 inline size_t fp8_flag_bytes(const Fp8Args& a) {
-    return (static_cast<size_t>((a.N + 15) / 16) * row_items(a, 16) * 8 + 255) / 256 * 256;
+    return (static_cast<size_t>((a.N + 15) / 16) * row_items(a, 16, false) * 8 + 255) / 256 * 256;
 }
 
 hipError_t launch_fp8_few(const Fp8Args& a, const Fp8Plan& p, bool gate_up, hipStream_t st);

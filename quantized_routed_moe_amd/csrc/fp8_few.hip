@@ -42,9 +42,9 @@ __device__ __forceinline__ void few_body(const Fp8Args& a, int n_tiles, float* p
     const int lane = threadIdx.x & 63, g = lane >> 4, col = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n_tile = blockIdx.x % n_tiles, item = blockIdx.x / n_tiles, n0 = n_tile * 16;
-    if (MATS == 1 && a.offsets && item == 0) zero_rows_past_end(a, n0, min(n0 + 16, a.N));
-    const RowItem it = row_item(a, item, 16);
+    const RowItem it = row_item(a, item, 16, MATS == 1);
     if (it.e < 0) return;
+    if (MATS == 1 && it.e == a.E) return zero_tile<16>(a, it, n0);
     const int S = ceil_div(a.K, kRun), NB = ceil_div(a.N, kRun);
     const int s_beg = S * wave / KW, s_end = S * (wave + 1) / KW;
 

@@ -346,15 +346,12 @@ __global__ __launch_bounds__(Tile<TN>::waves* kWave, 2) void fp8_tile_kernel(Fp8
     const int n_tile = (group * n_tiles >> group_bits) + at % per;      // n_tiles <= 2^24
     const int item = at / per * (8 >> group_bits) + (xcd >> group_bits);
     if (n_tile >= (group + 1) * n_tiles >> group_bits) return;
-    if constexpr (!GU) {
-        const int n0 = n_tile * TN;
-        if (a.offsets && item == 0) zero_rows_past_end(a, n0, min(n0 + TN, a.N));
-    }
     // offsets that overlap could make an item of the rounded-up grid's rest;
     // the workspace is sized for `items`
     if (item >= items) return;
-    const RowItem it = row_item(a, item, Tile<TN>::most_rows);
+    const RowItem it = row_item(a, item, Tile<TN>::most_rows, !GU);
     if (it.e < 0) return;
+    if (!GU && it.e == a.E) return zero_tile<TN>(a, it, n_tile * TN);
     const int rows = __builtin_amdgcn_readfirstlane(it.r1 - it.r0);
     if constexpr (TN == 256) {
         if (rows > 64) tile_body<TN, 2, 4, GU, BF>(a, it, n_tile, lds);

@@ -232,3 +232,39 @@ def test_grouped_gemm_of_more_columns_than_few_row_workgroups_fit():
             c = slice(n, min(n + 300, N))
             want, bound = R8.product(a[r], a_s[r], w[e, c].view(torch.float8_e4m3fn), w_s[e, n // 128:runs(c.stop)])
             R8.check_rounded(out[r, c], want, bound, F32)
+
+
+# ---------------------------------------------- rows past the last expert
+
+@pytest.mark.parametrize("out_dtype", [F32, BF16])
+@pytest.mark.parametrize("R,E,N,off", [
+    (1, 1, 50, [0, 0]), (9, 8, 271, [0, 0, 1, 1, 2, 2, 3, 4, 8]), (70, 64, 272, [0] + [1] * 64), (40, 2, 30, [0, 20, 39]),
+    (129, 1, 4096, [0, 1]), (700, 3, 1111, [0, 100, 101, 573]), (5000, 4, 1024, [0, 0, 64, 64, 129]),
+    (5000, 64, 4100, [0] + [i for i in range(64)]), (20000, 5, 2048, [0] * 6), (3000, 2, 77, [0, 1500, 2999])])
+def test_grouped_zeroes_rows_past_the_last_expert(R, E, N, off, out_dtype):
+    """On every path, rows that end inside a run, columns that end inside a
+    tile, and nothing behind the last row."""
+    K = 96
+    g = gen(R + N)
+    a, a_s, w, w_s = R8.codes(g, R, K), R8.scales(g, R, 1), R8.codes(g, E, N, K), R8.scales(g, E, runs(N), 1)
+    buf = torch.full((R * N + 4096,), 7.0, dtype=out_dtype, device="cuda")
+    out = buf[:R * N].view(R, N)
+    qm.grouped_gemm_fp8(a, a_s, w, w_s, torch.tensor(off, dtype=torch.int32, device="cuda"), out=out)
+    for e in range(E):
+        r = slice(off[e], off[e + 1])
+        if off[e + 1] > off[e]:
+            want, bound = R8.product(a[r], a_s[r], w[e], w_s[e])
+            R8.check_rounded(out[r], want, bound, out_dtype, f"expert {e}")
+    assert (out[off[-1]:] == 0).all() and (buf[R * N:] == 7).all()
+
+
+def test_grouped_time_of_rows_past_the_last_expert():
+    """64 live rows of 16384: about the time that zeros take (and less than
+    four times it), not the time of one workgroup that writes them in turn."""
+    R, E, N, K = 16384, 8, 4096, 256
+    g = gen(3)
+    a, a_s, w, w_s = R8.codes(g, R, K), R8.scales(g, R, 2), R8.codes(g, E, N, K), R8.scales(g, E, runs(N), 2)
+    off = torch.arange(E + 1, dtype=torch.int32, device="cuda") * 8
+    out = torch.empty((R, N), device="cuda")
+    us = [time_of(lambda: qm.grouped_gemm_fp8(a, a_s, w, w_s, off, out=out)), time_of(lambda: out.zero_())]
+    assert us[0] < 4 * us[1], us
