@@ -109,12 +109,13 @@ int moe_gemm_fp8(int32_t M, int32_t N, int32_t K, const uint8_t* a, int64_t a_st
    R sorted rows, E experts; a: [a_rows][K], w: E4M3 [E][N][K] with scales
    [E][ceil(N/128)][ceil(K/128)]; offsets int32 [E+1]; perm int32 [R] or NULL
    (then a_rows >= R); out [R][N], MOE_TYPE_F32 or MOE_TYPE_BF16, precision
-   as moe_gemm_fp8.  Rows at or past offsets[E] are written as zeros.
-   Experts without rows are not read.  Offsets outside [0, R] and rows
+   as moe_gemm_fp8.  Rows of no expert (from offsets[E] on, and below
+   offsets[0] where that is not 0) are written as zeros.  Experts without rows
+   are not read.  Offsets outside [0, R] and rows
    src(r) outside [0, a_rows) are clamped into range, never followed.
    Limits: R >= 0 (0 enqueues nothing), 1 <= E <= 64, N and K as
    moe_gemm_fp8, k >= 1, a_rows >= 1, workgroups as there with R / 128 +
-   min(E + 1, R) runs of rows.  Errors as moe_gemm_fp8. */
+   min(E + 2, R) runs of rows.  Errors as moe_gemm_fp8. */
 int moe_grouped_gemm_fp8(int32_t R, int32_t E, int32_t N, int32_t K, const uint8_t* a, int32_t a_rows,
                          const float* a_scales, const uint8_t* w, const float* w_scales, const int32_t* offsets,
                          const int32_t* perm, int32_t k, void* out, int32_t out_type, hipStream_t stream);
@@ -129,12 +130,12 @@ int moe_grouped_gemm_fp8(int32_t R, int32_t E, int32_t N, int32_t K, const uint8
    which is the `a` of a moe_grouped_gemm_fp8 with the down matrices (perm
    NULL).  gate, up: E4M3 [E][f][d] with scales [E][ceil(f/128)][ceil(d/128)];
    act E4M3 [T*k][f], act_scales fp32 [T*k][ceil(f/128)]; non-finite v as
-   moe_add_rmsnorm.  Rows at or past offsets[E] are left as they were.
+   moe_add_rmsnorm.  Rows of no expert are left as they were.
    ws: moe_expert_gate_up_fp8_workspace_bytes(shape) bytes (0: ws may be
    NULL), uninitialised; one call at a time.  Limits as include/moe.h
    (moe_shape) with d <= 2^22 (and f, in moe_layer_fp8), offsets and perm
    clamped as above, workgroups as there with tiles of 128
-   columns and no run past offsets[E].  Errors: as
+   columns and min(E, R).  Errors: as
    moe_expert_ffn. */
 size_t moe_expert_gate_up_fp8_workspace_bytes(const moe_shape* shape);
 int moe_expert_gate_up_fp8(const moe_shape* shape, const uint8_t* a, const float* a_scales, const uint8_t* gate,

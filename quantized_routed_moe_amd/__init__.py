@@ -812,7 +812,7 @@ def grouped_gemm_fp8(a, a_scales, w, w_scales, offsets, *, perm=None, k: int = 1
     """moe_grouped_gemm_fp8: sorted rows offsets[e] .. offsets[e+1] times
     w[e] ([E][N][K]); row r reads a[r], or a[perm[r] // k] with `perm` (int32,
     one entry per sorted row).  Returns out [rows][N], torch.float32 by
-    default (what moe_combine takes)."""
+    default (what moe_combine takes); rows of no expert are zeros."""
     dev = a.get_device()
     scope = _elsewhere(dev, stream, "grouped_gemm_fp8")
     if scope is not None:

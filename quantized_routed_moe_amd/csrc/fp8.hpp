@@ -34,20 +34,20 @@ struct Fp8Args {
     unsigned long long* flags;    // ... and a flag per workgroup
 };
 
-// Rows [r0, r1) of expert e; e = E: rows at or past offsets[E], to be zeroed;
-// e = -1 past the last item.
+// Rows [r0, r1) of expert e; e = E: rows of no expert, to be zeroed; e = -1
+// past the last item.
 struct RowItem {
     int e, r0, r1;
 };
 
 // Item idx of the schedule that cuts every expert's rows into runs of at
-// most `rows`, experts in id order, and after them (tail) the rows at or past
-// offsets[E], whose zeros so are spread over the grid as the products are (16384
-// rows x 4096 in fp32, 64 of them live: 41 us; by the workgroups of the first
-// item 1280).  Lane e of the calling wave reads expert e's bounds (clamped to
-// [0, R], so no offset is followed out of range) and a wave scan over the
-// experts' item counts finds the owner.  Uniform.
-__device__ __forceinline__ RowItem row_item(const Fp8Args& a, int idx, int rows, bool tail) {
+// most `rows`, experts in id order, and after them (rest) the rows of no expert,
+// below offsets[0] and from offsets[E] on, whose zeros so are spread over the
+// grid as the products are (16384 rows x 4096 in fp32, 64 of them live: 41 us; by
+// the workgroups of the first item 1280).  Lane e of the calling wave reads
+// expert e's bounds (clamped to [0, R], so no offset is followed out of range)
+// and a wave scan over the experts' item counts finds the owner.  Uniform.
+__device__ __forceinline__ RowItem row_item(const Fp8Args& a, int idx, int rows, bool rest) {
     if (!a.offsets) {
         const int r0 = idx * rows;
         return RowItem{r0 < a.R ? 0 : -1, r0, min(a.R, r0 + rows)};
@@ -67,10 +67,14 @@ __device__ __forceinline__ RowItem row_item(const Fp8Args& a, int idx, int rows,
     }
     const uint64_t hit = __ballot(idx >= incl - items && idx < incl);
     if (!hit) {
-        if (!tail) return RowItem{-1, 0, 0};
-        const long long r0 = min(max(a.offsets[a.E], 0), a.R) + static_cast<long long>(idx - lane_value(incl, 63)) * rows;
-        if (r0 >= a.R) return RowItem{-1, 0, 0};
-        return RowItem{a.E, static_cast<int>(r0), static_cast<int>(min(r0 + rows, static_cast<long long>(a.R)))};
+        if (!rest) return RowItem{-1, 0, 0};
+        const int head = min(max(a.offsets[0], 0), a.R), tail = min(max(a.offsets[a.E], head), a.R);
+        const int head_items = (head + rows - 1) / rows, at = idx - lane_value(incl, 63);
+        const long long r0 = at < head_items ? static_cast<long long>(at) * rows
+                                             : tail + static_cast<long long>(at - head_items) * rows;
+        const int r1 = at < head_items ? head : a.R;
+        if (r0 >= r1) return RowItem{-1, 0, 0};
+        return RowItem{a.E, static_cast<int>(r0), static_cast<int>(min(r0 + rows, static_cast<long long>(r1)))};
     }
     const int e = __ffsll(static_cast<unsigned long long>(hit)) - 1;
     const int r0 = lane_value(lo, e) + (idx - lane_value(incl - items, e)) * rows;
@@ -78,9 +82,9 @@ __device__ __forceinline__ RowItem row_item(const Fp8Args& a, int idx, int rows,
 }
 
 // Upper bound of the items of any sound offsets.
-inline long long row_items(const Fp8Args& a, int rows, bool tail) {
+inline long long row_items(const Fp8Args& a, int rows, bool rest) {
     if (!a.offsets) return (static_cast<long long>(a.R) + rows - 1) / rows;
-    const int groups = a.E + tail;
+    const int groups = a.E + (rest ? 2 : 0);
     return a.R / rows + (groups < a.R ? groups : a.R);
 }
 

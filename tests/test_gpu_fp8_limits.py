@@ -268,3 +268,21 @@ def test_grouped_time_of_rows_past_the_last_expert():
     out = torch.empty((R, N), device="cuda")
     us = [time_of(lambda: qm.grouped_gemm_fp8(a, a_s, w, w_s, off, out=out)), time_of(lambda: out.zero_())]
     assert us[0] < 4 * us[1], us
+
+
+@pytest.mark.parametrize("out_dtype", [F32, BF16])
+@pytest.mark.parametrize("R,N,off", [(9, 271, [4, 6, 8]), (1, 40, [1, 1]), (600, 1111, [130, 130, 300, 599]),
+                                     (5000, 1024, [4000, 4100, 5000]), (5000, 1024, [129, 129, 260]), (300, 64, [300] * 3)])
+def test_grouped_rows_below_the_first_offset_are_zero(R, N, off, out_dtype):
+    """The experts of one part of a dispatch: offsets that do not begin at 0."""
+    E, K = len(off) - 1, 160
+    g = gen(R + N)
+    a, a_s, w, w_s = R8.codes(g, R, K), R8.scales(g, R, 2), R8.codes(g, E, N, K), R8.scales(g, E, runs(N), 2)
+    out = torch.full((R, N), float("nan"), dtype=out_dtype, device="cuda")
+    qm.grouped_gemm_fp8(a, a_s, w, w_s, torch.tensor(off, dtype=torch.int32, device="cuda"), out=out)
+    for e in range(E):
+        r = slice(off[e], off[e + 1])
+        if off[e + 1] > off[e]:
+            want, bound = R8.product(a[r], a_s[r], w[e], w_s[e])
+            R8.check_rounded(out[r], want, bound, out_dtype, f"expert {e}")
+    assert (out[:off[0]] == 0).all() and (out[off[-1]:] == 0).all()
