@@ -286,3 +286,67 @@ def test_grouped_rows_below_the_first_offset_are_zero(R, N, off, out_dtype):
             want, bound = R8.product(a[r], a_s[r], w[e], w_s[e])
             R8.check_rounded(out[r], want, bound, out_dtype, f"expert {e}")
     assert (out[:off[0]] == 0).all() and (out[off[-1]:] == 0).all()
+
+
+# ------------------------------------- non-finite values of gate/up's output
+
+GATE_UP_PATHS = [(3, 2, 1, 256), (100, 8, 2, 1056), (900, 4, 2, 2048)]      # T, E, k, f: 16, 32 and 128 columns a workgroup
+
+
+@pytest.mark.parametrize("T,E,k,f", GATE_UP_PATHS)
+def test_gate_up_of_nan_codes(T, E, k, f):
+    """A NaN in a token makes its rows NaN, one in a weight row that column of
+    the expert; a NaN does not enter its run's maximum, so every other code
+    and scale is what it is without that column."""
+    d = 160
+    g = gen(T)
+    off, perm, _ = R8.routing(g, T, E, k)
+    a, a_s = R8.codes(g, T, d), R8.scales(g, T, 2, mean=2.0 ** -6)
+    gate, up = R8.codes(g, E, f, d), R8.codes(g, E, f, d)
+    gs, us = R8.scales(g, E, runs(f), 2), R8.scales(g, E, runs(f), 2)
+    ua, ug, uu = (t.view(torch.uint8).clone() for t in (a, gate, up))
+    bad = T // 2
+    n0, n1 = f - 20, 37
+    uu0 = uu.clone()
+    uu0[:, n0] = 0                       # v = 0 there: does not enter the maximum either
+    uu0[:, n1] = 0
+    want, want_s = qm.expert_gate_up_fp8(ua, a_s, ug, gs, uu0, us, off, perm, k)
+    ua[bad, 159], ug[:, n0, 3], uu[:, n1, 131] = 0x7F, 0xFF, 0x7F
+    q, sc = qm.expert_gate_up_fp8(ua, a_s, ug, gs, uu, us, off, perm, k)
+    q, want = q.view(torch.float8_e4m3fn).float(), want.view(torch.float8_e4m3fn).float()
+    rows = perm.long() // k == bad
+    assert rows.sum() == k and torch.isnan(q[rows]).all() and (sc[rows] == R8.SCALE_MIN).all()
+    col = torch.zeros(f, dtype=torch.bool, device="cuda")
+    col[n0] = col[n1] = True
+    assert torch.isnan(q[:, col]).all()
+    assert torch.equal(q[~rows][:, ~col], want[~rows][:, ~col]) and torch.equal(sc[~rows], want_s[~rows])
+
+
+@pytest.mark.parametrize("T,E,k,f", GATE_UP_PATHS)
+def test_gate_up_of_overflowing_values(T, E, k, f):
+    """up overflows to an infinity in one column of a run whose other values
+    are 0: scale infinite, code NaN there and 0 beside it; the other runs are
+    not touched."""
+    d = 128
+    g = gen(T + 1)
+    off, perm, _ = R8.routing(g, T, E, k)
+    a, a_s = R8.codes(g, T, d).float().abs().add(16).clamp(max=448).to(torch.float8_e4m3fn), torch.full((T, 1), 2.0 ** -6, device="cuda")
+    gate, up = (R8.codes(g, E, f, d).float().abs().add(16).clamp(max=448).to(torch.float8_e4m3fn) for _ in range(2))
+    gs, us = (torch.full((E, runs(f), 1), 2.0 ** -9, device="cuda") for _ in range(2))
+    want, want_s = qm.expert_gate_up_fp8(a, a_s, gate, gs, up, us, off, perm, k)
+    b, n = 1, 128 + 77
+    uu = up.view(torch.uint8).clone()
+    uu[:, 128:256] = 0
+    uu[:, n] = up.view(torch.uint8)[:, n]
+    us[:, b] = 3e38
+    q, sc = qm.expert_gate_up_fp8(a, a_s, gate, gs, uu, us, off, perm, k)
+    qf, wf = q.float(), want.float()
+    assert torch.isinf(sc[:, b]).all() and torch.isnan(qf[:, n]).all()
+    run = torch.zeros(f, dtype=torch.bool, device="cuda")
+    run[128:256] = True
+    others = run.clone()
+    others[n] = False
+    assert (qf[:, others] == 0).all()
+    assert torch.equal(qf[:, ~run], wf[:, ~run])
+    keep = torch.arange(sc.shape[1], device="cuda") != b
+    assert torch.equal(sc[:, keep], want_s[:, keep])
