@@ -49,8 +49,14 @@ __global__ void clear_header_kernel(uint32_t* header) {
 hipError_t launch_combine(const moe_shape& s, const float* y, const int32_t* inv, const float* w,
                           float* out, hipStream_t st, bool shared) {
     const float* ys = shared ? y + static_cast<size_t>(s.T) * s.k * s.d : nullptr;
-    combine_kernel<<<s.T, 256, 0, st>>>(y, inv, w, out, s.d, s.k, ys);
-    return hipGetLastError();
+    constexpr int kMost = 1 << 23;       // tokens of a launch: a grid holds fewer than 2^32 threads
+    for (long long t = 0; t < s.T; t += kMost) {
+        const int n = static_cast<int>(s.T - t < kMost ? s.T - t : kMost);
+        combine_kernel<<<n, 256, 0, st>>>(y, inv + t * s.k, w + t * s.k, out + t * s.d, s.d, s.k, ys ? ys + t * s.d : nullptr);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 hipError_t launch_clear_header(uint32_t* header, hipStream_t st) {

@@ -350,3 +350,19 @@ def test_gate_up_of_overflowing_values(T, E, k, f):
     assert torch.equal(qf[:, ~run], wf[:, ~run])
     keep = torch.arange(sc.shape[1], device="cuda") != b
     assert torch.equal(sc[:, keep], want_s[:, keep])
+
+
+# ------------------------------------------ a layer of 2^24 tokens and more
+
+def test_layer_of_more_tokens_than_a_grid_of_256_threads_holds():
+    T, d, E, k, f = (1 << 24) + 3, 32, 2, 1, 32
+    q, sc, ex, lg = layer_case(T, d, E, k, f, seed=11)
+    out, ids, tw, _ = qm.layer_fp8(None, q, sc, ex, k, logits=lg, check=True)
+    assert torch.equal(ids[:, 0].long(), lg.argmax(1)) and (tw == 1).all()
+    perm = torch.sort(ids[:, 0].long(), stable=True).indices
+    off = torch.cat([ids.new_zeros(1), torch.bincount(ids[:, 0].long(), minlength=E).cumsum(0).to(torch.int32)])
+    act, acts = qm.expert_gate_up_fp8(q, sc, ex.gate, ex.gate_scales, ex.up, ex.up_scales, off, perm.to(torch.int32), k)
+    y = qm.grouped_gemm_fp8(act, acts, ex.down, ex.down_scales, off)
+    want = torch.empty_like(y)
+    want[perm] = y
+    assert torch.equal(out, want)
