@@ -114,8 +114,8 @@ int moe_gemm_fp8(int32_t M, int32_t N, int32_t K, const uint8_t* a, int64_t a_st
    are not read.  Offsets outside [0, R] and rows
    src(r) outside [0, a_rows) are clamped into range, never followed.
    Limits: R >= 0 (0 enqueues nothing), 1 <= E <= 64, N and K as
-   moe_gemm_fp8, k >= 1, a_rows >= 1, workgroups as there with R / 128 +
-   min(E + 2, R) runs of rows.  Errors as moe_gemm_fp8. */
+   moe_gemm_fp8, k >= 1, a_rows >= 1, workgroups as there with at most
+   (R + 127 min(E + 2, R)) / 128 runs of rows.  Errors as moe_gemm_fp8. */
 int moe_grouped_gemm_fp8(int32_t R, int32_t E, int32_t N, int32_t K, const uint8_t* a, int32_t a_rows,
                          const float* a_scales, const uint8_t* w, const float* w_scales, const int32_t* offsets,
                          const int32_t* perm, int32_t k, void* out, int32_t out_type, hipStream_t stream);
@@ -135,7 +135,7 @@ int moe_grouped_gemm_fp8(int32_t R, int32_t E, int32_t N, int32_t K, const uint8
    NULL), uninitialised; one call at a time.  Limits as include/moe.h
    (moe_shape) with d <= 2^22 (and f, in moe_layer_fp8), offsets and perm
    clamped as above, workgroups as there with tiles of 128
-   columns and min(E, R).  Errors: as
+   columns and E for E + 2.  Errors: as
    moe_expert_ffn. */
 size_t moe_expert_gate_up_fp8_workspace_bytes(const moe_shape* shape);
 int moe_expert_gate_up_fp8(const moe_shape* shape, const uint8_t* a, const float* a_scales, const uint8_t* gate,

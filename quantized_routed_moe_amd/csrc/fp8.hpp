@@ -84,8 +84,8 @@ __device__ __forceinline__ RowItem row_item(const Fp8Args& a, int idx, int rows,
 // Upper bound of the items of any sound offsets.
 inline long long row_items(const Fp8Args& a, int rows, bool rest) {
     if (!a.offsets) return (static_cast<long long>(a.R) + rows - 1) / rows;
-    const int groups = a.E + (rest ? 2 : 0);
-    return a.R / rows + (groups < a.R ? groups : a.R);
+    const long long groups = a.E + (rest ? 2 : 0);
+    return (a.R + (groups < a.R ? groups : a.R) * (rows - 1)) / rows;      // each group's last run as short as can be
 }
 
 // Row of `a` that sorted row r reads.
@@ -208,7 +208,8 @@ struct Fp8Plan {
     Fp8Path path;
     int cols, rows, n_tiles;
     int group_bits;       // kMid, kMany: 2^group_bits groups of column tiles are dealt to the XCDs
-    int items;            // upper bound; the grid may be rounded up beyond it
+    int items;            // upper bound, with those of no expert's rows; the grid may be rounded up beyond it
+    int products;         // upper bound of those that have a product to do
     long long blocks;
 };
 
@@ -244,11 +245,12 @@ inline Fp8Plan fp8_plan(const Fp8Args& a, bool gate_up) {
     p.rows = p.path == Fp8Path::kFew ? 16 : p.path == Fp8Path::kMid ? 64 : 128;
     p.n_tiles = (a.N + p.cols - 1) / p.cols;
     p.items = static_cast<int>(row_items(a, p.rows, !gate_up));
+    p.products = static_cast<int>(row_items(a, p.rows, false));
     // Four groups of column tiles where they come out even, and as many as it
-    // takes that no XCD is without an item (17 x 128256 x 4096, 501 tiles of one
+    // takes that no XCD is without a product (17 x 128256 x 4096, 501 tiles of one
     // item: 128 us, with one group, that is on one XCD, 500).
     p.group_bits = p.n_tiles % 4 == 0 ? 2 : p.n_tiles % 2 == 0 ? 1 : 0;
-    while ((8 >> p.group_bits) > p.items) ++p.group_bits;
+    while ((8 >> p.group_bits) > p.products) ++p.group_bits;
     const int groups = 1 << p.group_bits, classes = 8 / groups, per = (p.n_tiles + groups - 1) / groups;
     p.blocks = p.path == Fp8Path::kFew ? static_cast<long long>(p.n_tiles) * p.items
                                        : 8ll * per * ((p.items + classes - 1) / classes);

@@ -132,7 +132,7 @@ __global__ __launch_bounds__(KW* kWave) void fp8_few_kernel(Fp8Args a, int n_til
 // 23 experts of 4096 x 2048: 45, 40).
 hipError_t launch_fp8_few(const Fp8Args& a, const Fp8Plan& p, bool gate_up, hipStream_t st) {
     const int blocks = static_cast<int>(p.blocks);
-    const bool eight = ceil_div(a.K, kRun) >= 24 || blocks <= 256;
+    const bool eight = ceil_div(a.K, kRun) >= 24 || static_cast<long long>(p.n_tiles) * p.products <= 256;
     if (gate_up && eight) fp8_few_kernel<2, 8><<<blocks, 8 * kWave, 0, st>>>(a, p.n_tiles);
     else if (gate_up) fp8_few_kernel<2, 4><<<blocks, 4 * kWave, 0, st>>>(a, p.n_tiles);
     else if (eight) fp8_few_kernel<1, 8><<<blocks, 8 * kWave, 0, st>>>(a, p.n_tiles);

@@ -366,3 +366,15 @@ def test_layer_of_more_tokens_than_a_grid_of_256_threads_holds():
     want = torch.empty_like(y)
     want[perm] = y
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("out_dtype", [F32, BF16])
+@pytest.mark.parametrize("R,N,K", [(1, 4096, 2048), (4, 4096, 2048), (16, 4096, 1024), (40, 4096, 2048), (500, 1024, 512)])
+def test_grouped_of_one_expert_is_the_dense_product(R, N, K, out_dtype):
+    """The same kernel and the same order of sums: items that could hold rows
+    of no expert change nothing."""
+    g = gen(R)
+    a, a_s, w, w_s = R8.codes(g, R, K), R8.scales(g, R, runs(K)), R8.codes(g, N, K), R8.scales(g, runs(N), runs(K))
+    off = torch.tensor([0, R], dtype=torch.int32, device="cuda")
+    got = qm.grouped_gemm_fp8(a, a_s, w[None], w_s[None], off, out_dtype=out_dtype)
+    assert torch.equal(got, qm.gemm_fp8(a, a_s, w, w_s, out_dtype=out_dtype))
