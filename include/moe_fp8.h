@@ -95,8 +95,8 @@ int moe_add_rmsnorm(int32_t T, int32_t d, const void* x, int32_t x_type, int64_t
    Limits: M >= 0 (0 enqueues nothing), N >= 1, both below 2^30; K a positive
    multiple of 32 up to 2^22; the workgroups, one per tile of 128 rows x 256
    columns and some that make the rounds over eight XCDs whole, fewer than 2^23
-   (fewer than 2^22 tiles always fit).  Errors: MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_ERR_FORMAT,
-   MOE_ERR_ALIGN, MOE_ERR_HIP. */
+   (fewer than 2^22 tiles always fit).  Errors: MOE_ERR_NULL, MOE_ERR_SHAPE,
+   MOE_ERR_FORMAT, MOE_ERR_ALIGN, MOE_ERR_HIP. */
 int moe_gemm_fp8(int32_t M, int32_t N, int32_t K, const uint8_t* a, int64_t a_stride, const float* a_scales,
                  const uint8_t* w, const float* w_scales, void* out, int32_t out_type, int64_t out_stride,
                  hipStream_t stream);
@@ -111,8 +111,8 @@ int moe_gemm_fp8(int32_t M, int32_t N, int32_t K, const uint8_t* a, int64_t a_st
    (then a_rows >= R); out [R][N], MOE_TYPE_F32 or MOE_TYPE_BF16, precision
    as moe_gemm_fp8.  Rows of no expert (from offsets[E] on, and below
    offsets[0] where that is not 0) are written as zeros.  Experts without rows
-   are not read.  Offsets outside [0, R] and rows
-   src(r) outside [0, a_rows) are clamped into range, never followed.
+   are not read.  Offsets outside [0, R] and rows src(r) outside [0, a_rows) are
+   clamped into range, never followed.
    Limits: R >= 0 (0 enqueues nothing), 1 <= E <= 64, N and K as
    moe_gemm_fp8, k >= 1, a_rows >= 1, workgroups as there with at most
    (R + 127 min(E + 2, R)) / 128 runs of rows.  Errors as moe_gemm_fp8. */
@@ -133,10 +133,9 @@ int moe_grouped_gemm_fp8(int32_t R, int32_t E, int32_t N, int32_t K, const uint8
    moe_add_rmsnorm.  Rows of no expert are left as they were.
    ws: moe_expert_gate_up_fp8_workspace_bytes(shape) bytes (0: ws may be
    NULL), uninitialised; one call at a time.  Limits as include/moe.h
-   (moe_shape) with d <= 2^22 (and f, in moe_layer_fp8), offsets and perm
-   clamped as above, workgroups as there with tiles of 128
-   columns and E for E + 2.  Errors: as
-   moe_expert_ffn. */
+   (moe_shape) with d <= 2^22 (and f, in moe_layer_fp8), workgroups as above
+   with tiles of 128 columns and E for E + 2; offsets and perm clamped as above.
+   Errors as moe_expert_ffn. */
 size_t moe_expert_gate_up_fp8_workspace_bytes(const moe_shape* shape);
 int moe_expert_gate_up_fp8(const moe_shape* shape, const uint8_t* a, const float* a_scales, const uint8_t* gate,
                            const float* gate_scales, const uint8_t* up, const float* up_scales,

@@ -12,9 +12,9 @@
 // chunks l/16 and 4 + l/16 of row l%16's 128 bytes, so the two loads of a step
 // consume 16 whole cache lines.  What keeps enough on its way is the number of
 // waves (up to 32 a CU), not requests ahead in each: one row x 4096 x 4096 takes
-// 6.0 us (2.7 of them a launch of any size), 25 experts of 4096 x 2048 with a
+// 5.4 us (2.7 of them a launch of any size), 25 experts of 4096 x 2048 with a
 // row or two each 40 us, the weights at 5.3 TB/s; with two chunks of two steps
-// held ahead 6.9 and 65 us.
+// held ahead, both built for one run, 6.9 beside 6.0 and 65 beside 40.
 //
 // Operands are bf16 (E4M3 converts exactly) on the 16x16x32 instruction: the
 // fp8 instructions align their products before adding (1.5e-5 relative per
@@ -126,8 +126,8 @@ __global__ __launch_bounds__(KW* kWave) void fp8_few_kernel(Fp8Args a, int n_til
 
 }  // namespace
 
-// Eight waves where each has three steps or more (32 steps, 1 x 4096 x 4096:
-// eight 5.9 us, four 7.2; gate/up, 29 experts: 91, 95) or there is no more than
+// Eight waves where each has three steps or more (32 steps, 1 x 4096 x 4096, in
+// one run: eight 5.9 us, four 7.2; gate/up, 29 experts: 91, 95) or there is no more than
 // one workgroup a CU (16 steps, 1 x 4096 x 2048: 4.3, 4.9); else four (16 steps,
 // 23 experts of 4096 x 2048: 45, 40).
 hipError_t launch_fp8_few(const Fp8Args& a, const Fp8Plan& p, bool gate_up, hipStream_t st) {

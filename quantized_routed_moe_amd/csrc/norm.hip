@@ -10,8 +10,8 @@
 // holds 8 consecutive values per chunk, so a run of 128 is 16 neighbouring
 // lanes and its maximum four lane exchanges.  Few rows are bound by the length
 // of a thread's work, mostly the divisions of its codes: the row is spread over
-// as many threads as it has chunks (1 x 4096: 4.1 us, with two chunks a thread
-// 5.3; a launch of any size is 2.7).
+// as many threads as it has chunks (1 x 4096: 3.5 us, of which a launch of any
+// size is 2.7; with two chunks a thread, in one run, 5.3 beside 4.1).
 #include "fp8.hpp"
 #include "kernels.hpp"
 
