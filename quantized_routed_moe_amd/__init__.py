@@ -1,5 +1,6 @@
 """Python binding of the routed MoE layer's C ABI (``include/moe.h``, the FP8
-operators of ``include/moe_fp8.h``, and the roofline measurement kernels of
+operators of ``include/moe_fp8.h``, those of a batch of many requests of
+``include/moe_batch.h``, and the roofline measurement kernels of
 ``include/moe_peak.h``).
 
 Argument marshalling only: every step of the layer runs in the HIP kernels of
@@ -64,6 +65,9 @@ EXPORTS = (
     # include/moe_fp8.h
     "moe_add_rmsnorm", "moe_gemm_fp8", "moe_grouped_gemm_fp8", "moe_expert_gate_up_fp8_workspace_bytes",
     "moe_expert_gate_up_fp8", "moe_layer_fp8_workspace_bytes", "moe_layer_fp8",
+    # include/moe_batch.h
+    "moe_lora_items", "moe_lora_plan_workspace_bytes", "moe_lora_plan", "moe_lora_add_workspace_bytes", "moe_lora_add",
+    "moe_token_logprobs_workspace_bytes", "moe_token_logprobs",
     # include/moe_peak.h
     "moe_peak_stream", "moe_peak_mfma", "moe_peak_hold",
 )
@@ -163,6 +167,13 @@ def lib() -> ctypes.CDLL:
             "moe_expert_gate_up_fp8": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
             "moe_layer_fp8_workspace_bytes": (_SZ, [_P]),
             "moe_layer_fp8": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+            "moe_lora_items": (_SZ, [_I, _I]),
+            "moe_lora_plan_workspace_bytes": (_SZ, [_I, _I]),
+            "moe_lora_plan": (_I, [_I, _I, _P, _P, _P, _P, _P, _SZ, _P]),
+            "moe_lora_add_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I]),
+            "moe_lora_add": (_I, [_I, _I, _I, _I, _I, _P, _I64, _P, _P, _P, _P, _P, _P, _I64, _P, _I64, _I, _P, _SZ, _P]),
+            "moe_token_logprobs_workspace_bytes": (_SZ, [_I, _I, _I]),
+            "moe_token_logprobs": (_I, [_I, _I, _P, _I, _I64, _P, _I, _P, _P, _I, _P, _P, _P, _SZ, _P]),
             "moe_peak_stream": (_I, [_P, _SZ, ctypes.c_int32, _P, _P]),
             "moe_peak_mfma": (_I, [ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, _P, _P]),
             "moe_peak_hold": (_I, [ctypes.c_uint32, _P]),
@@ -985,6 +996,150 @@ def layer_fp8(x, xq, xq_scales, experts: ExpertsFp8, k: int, *, w_router=None, b
     if check:
         check_device_status(ws, "layer_fp8")
     return out, ids, w, logits
+
+
+# ------------------------------------------- a batch of many requests
+
+@dataclass
+class LoraPlan:
+    """A batch's tokens by adapter (moe_lora_plan): perm int32 [T], offsets
+    int32 [adapters + 2], items int32 [...][4]."""
+    T: int
+    adapters: int
+    perm: object
+    offsets: object
+    items: object
+
+
+def lora_plan(ids, adapters: int, *, stream=None) -> LoraPlan:
+    """moe_lora_plan: groups the tokens of a batch by adapter (ids int32 [T];
+    an id outside [0, adapters) is a token of no adapter), once for all the
+    lora_add calls of a step."""
+    dev = ids.get_device()
+    scope = _elsewhere(dev, stream, "lora_plan")
+    if scope is not None:
+        with scope:
+            return lora_plan(ids, adapters)
+    torch = _torch()
+    T = ids.numel()
+    idp = _addr(ids, (torch.int32,), (T,), dev, "ids")
+    L = lib()
+    n = L.moe_lora_items(T, adapters)
+    if T and not n:
+        raise MoeError(MOE_ERR_SHAPE, "moe_lora_plan")
+    # one allocation: items first, for their alignment
+    new = ids.new_empty if T else ids.new_zeros
+    buf = new(4 * n + T + adapters + 2)
+    perm, offsets = buf[4 * n:4 * n + T], buf[4 * n + T:]
+    nw = L.moe_lora_plan_workspace_bytes(T, adapters)
+    ws = ids.new_empty(nw // 4) if nw else None
+    p = buf.data_ptr()
+    rc = L.moe_lora_plan(T, adapters, idp, p + 4 * (4 * n + T), p + 16 * n, p, None if ws is None else ws.data_ptr(), nw,
+                         _raw_stream(dev))
+    if rc:
+        raise MoeError(rc, "moe_lora_plan")
+    return LoraPlan(T, adapters, perm, offsets, buf[:4 * n].view(n, 4))
+
+
+def lora_add(base, x, a, b, plan: LoraPlan, *, scales=None, out=None, ws=None, stream=None):
+    """moe_lora_add: base [T][N] (bf16 or fp32, a shared projection's result)
+    plus, for each token of an adapter g of the plan, scales[g] * b[g] a[g] x:
+    x bf16 [T][K], a bf16 [L][r][K], b bf16 [L][N][r], scales fp32 [L] (1 by
+    default).  base's, x's and out's rows may lie apart.  `out` takes the
+    result (it may be `base`: in place); by default a new tensor.  ws: a uint8
+    tensor of moe_lora_add_workspace_bytes, allocated by default.  Returns
+    out."""
+    dev = base.get_device()
+    scope = _elsewhere(dev, stream, "lora_add")
+    if scope is not None:
+        with scope:
+            return lora_add(base, x, a, b, plan, scales=scales, out=out, ws=ws)
+    torch = _torch()
+    bf16, i32 = (torch.bfloat16,), (torch.int32,)
+    T, N = shape = base.shape
+    L, r, K = a.shape
+    if x.dtype != torch.bfloat16 or x.shape != (T, K):
+        raise ValueError(f"x must be torch.bfloat16 of shape {(T, K)}")
+    if plan.T != T or plan.adapters != L:
+        raise ValueError(f"the plan is of {plan.T} tokens and {plan.adapters} adapters, not {T} and {L}")
+    xp, xs = _rows(x, dev, "x")
+    bp, bs = _rows(base, dev, "base")
+    bt = _moe_type(base.dtype, "base")
+    ap = _addr(a, bf16, (L, r, K), dev, "a")
+    bbp = _addr(b, bf16, (L, N, r), dev, "b")
+    sp = None if scales is None else _addr(scales, (torch.float32,), (L,), dev, "scales")
+    pp = _addr(plan.perm, i32, (T,), dev, "plan.perm")
+    if plan.items.get_device() != dev:
+        raise ValueError(f"the plan is on {plan.items.device}, not on device {dev}")
+    if out is None:
+        out = torch.empty_like(base, memory_format=torch.contiguous_format)
+        op, os_ = out.data_ptr(), N
+    else:
+        if out.shape != shape or out.dtype != base.dtype:
+            raise ValueError("out must have base's shape and dtype")
+        op, os_ = _rows(out, dev, "out")
+    lb = lib()
+    if ws is None:
+        n = lb.moe_lora_add_workspace_bytes(T, K, N, r, L)
+        ws = base.new_empty(n, dtype=torch.uint8) if n else None
+    else:
+        n = ws.numel() * ws.element_size()
+        if ws.get_device() != dev:
+            raise ValueError(f"ws is on {ws.device}, not on device {dev}")
+    rc = lb.moe_lora_add(T, K, N, r, L, xp, xs, ap, bbp, sp, pp, plan.items.data_ptr(), bp, bs, op, os_, bt,
+                         None if ws is None else _ptr(ws, name="ws"), n, _raw_stream(dev))
+    if rc:
+        raise MoeError(rc, "moe_lora_add")
+    return out
+
+
+def token_logprobs(logits, tokens=None, *, top: int = 0, entropy: bool = False, ws=None, stream=None):
+    """moe_token_logprobs on rows of logits [T][V] (bf16 or fp32, rows may lie
+    apart): the log probabilities of tokens (int32 [T] or [T][n]), each row's
+    entropy, and the `top` likeliest tokens (ties to the lower id) with their
+    log probabilities.  ws: a uint8 tensor of
+    moe_token_logprobs_workspace_bytes, allocated by default.  Returns
+    (logprobs, entropy, top_ids, top_logprobs), None for what was not asked."""
+    dev = logits.get_device()
+    scope = _elsewhere(dev, stream, "token_logprobs")
+    if scope is not None:
+        with scope:
+            return token_logprobs(logits, tokens, top=top, entropy=entropy, ws=ws)
+    torch = _torch()
+    f32, i32 = torch.float32, torch.int32
+    lp, stride = _rows(logits, dev, "logits")
+    T, V = logits.shape
+    lt = _moe_type(logits.dtype, "logits")
+    out = ent = ids = top_lp = None
+    tp = outp = entp = idp = tlp = None
+    given = 0
+    if tokens is not None:
+        if tokens.dim() not in (1, 2) or tokens.shape[0] != T:
+            raise ValueError(f"tokens must have shape ({T},) or ({T}, n)")
+        given = 1 if tokens.dim() == 1 else tokens.shape[1]
+        tp = _addr(tokens, (i32,), tokens.shape, dev, "tokens")
+        out = torch.empty_like(tokens, dtype=f32)
+        outp = out.data_ptr()
+    if entropy:
+        ent = logits.new_empty(T, dtype=f32)
+        entp = ent.data_ptr()
+    if top:
+        ids = logits.new_empty((T, top), dtype=i32)
+        top_lp = logits.new_empty((T, top), dtype=f32)
+        idp, tlp = ids.data_ptr(), top_lp.data_ptr()
+    lb = lib()
+    if ws is None:
+        n = lb.moe_token_logprobs_workspace_bytes(T, V, top)
+        ws = logits.new_empty(n, dtype=torch.uint8) if n else None
+    else:
+        n = ws.numel() * ws.element_size()
+        if ws.get_device() != dev:
+            raise ValueError(f"ws is on {ws.device}, not on device {dev}")
+    rc = lb.moe_token_logprobs(T, V, lp, lt, stride, tp, given, outp, entp, top, idp, tlp,
+                               None if ws is None else _ptr(ws, name="ws"), n, _raw_stream(dev))
+    if rc:
+        raise MoeError(rc, "moe_token_logprobs")
+    return out, ent, ids, top_lp
 
 
 # ------------------------------------------------------------------ slot bank
