@@ -1,6 +1,8 @@
 // Entry points of the operators of a batch of many requests: argument checks
 // (all on the host, before any HIP call) and launches.  See
 // include/moe_batch.h for the contract.
+#include <algorithm>
+
 #include "../../include/moe_batch.h"
 #include "batch.hpp"
 #include "validate.hpp"
@@ -35,9 +37,10 @@ bool scores_ok(int T, int V, int top) {
     return T >= 0 && T < kDimLimit && V >= 1 && V < kDimLimit && top >= 0 && top <= kMostTop && top <= V;
 }
 
+// The parts of either type: what a caller allocates serves both.
 size_t scores_ws(int T, int V, int top) {
-    const int parts = T ? score_parts(T, V) : 1;
-    return parts > 1 ? score_stat_bytes(T, parts) + (static_cast<size_t>(T) * parts * top * 8 + 255) / 256 * 256 : 0;
+    const int parts = T ? std::max(score_parts(T, V, true), score_parts(T, V, false)) : 1;
+    return parts > 1 ? score_stat_bytes(T, parts) + (static_cast<size_t>(T) * parts * (top + 1) * 8 + 255) / 256 * 256 : 0;
 }
 
 int check_ws(const void* ws, size_t ws_bytes, size_t need) {
@@ -115,7 +118,7 @@ int moe_lora_add(int32_t T, int32_t K, int32_t N, int32_t r, int32_t L, const ui
     p.out_stride = out_stride;
     p.f32 = type == MOE_TYPE_F32;
     const int per = p.f32 ? 4 : 8;
-    p.vec = base_stride % per == 0 && out_stride % per == 0;
+    p.vec = N % 8 == 0 && base_stride % per == 0 && out_stride % per == 0;
     p.in_place = base == out;
     p.splits = lora_splits(T, K, r, L);
     p.v = static_cast<float*>(ws);
@@ -141,13 +144,16 @@ int moe_token_logprobs(int32_t T, int32_t V, const void* logits, int32_t type, i
         return MOE_ERR_ALIGN;
     const int rc = check_ws(ws, ws_bytes, scores_ws(T, V, top));
     if (rc != MOE_OK) return rc;
-    ScoreArgs p{T, V, given, top, score_parts(T, V), logits, stride, tokens, logprobs, entropy, top_logprobs, top_ids,
-                nullptr, nullptr};
+    const bool f32 = type == MOE_TYPE_F32;
+    const int parts = score_parts(T, V, f32);
+    ScoreArgs p{T, V, given, top, parts, score_take(T, V, top, f32, parts), logits, stride, tokens, logprobs, entropy, top_logprobs, top_ids,
+                nullptr, nullptr, nullptr};
     if (p.parts > 1) {
         p.stats = static_cast<float*>(ws);
-        p.keys = reinterpret_cast<unsigned long long*>(static_cast<char*>(ws) + score_stat_bytes(T, p.parts));
+        p.flags = reinterpret_cast<unsigned long long*>(static_cast<char*>(ws) + score_stat_bytes(T, p.parts));
+        p.keys = p.flags + static_cast<size_t>(T) * p.parts;
     }
-    return hip_rc(launch_scores(p, type == MOE_TYPE_F32, stream));
+    return hip_rc(launch_scores(p, f32, stream));
 }
 
 }  // extern "C"

@@ -47,7 +47,7 @@ struct LoraArgs {
     void* out;
     long long base_stride, out_stride;
     int f32;                                   // 1: base and out are fp32, 0: bf16
-    int vec;                                   // 1: whole 16 bytes of base and out can be moved at once
+    int vec;                                   // 1: eight columns of base and out lie in whole 16 bytes, N is a multiple of 8
     int in_place;
     int splits;                                // parts of K
     float* v;                                  // [splits][T][r], by entry of perm
@@ -60,8 +60,16 @@ hipError_t launch_lora_add(const LoraArgs& a, hipStream_t st);
 
 // ---- scores
 
+// What a workgroup takes (scores.hip).
+enum class ScoreTake {
+    kRows,   // a row a wave
+    kRow,    // a row
+    kPart    // a part of a row, or a short one, seen twice
+};
+
 struct ScoreArgs {
     int T, V, given, top, parts;
+    ScoreTake take;
     const void* logits;
     long long stride;
     const int32_t* tokens;
@@ -69,9 +77,11 @@ struct ScoreArgs {
     int32_t* top_ids;
     float* stats;                              // parts > 1: [T][parts][4] maximum, sum, weighted sum
     unsigned long long* keys;                  // [T][parts][top]
+    unsigned long long* flags;                 // [T][parts]
 };
 
-int score_parts(int T, int V);
+int score_parts(int T, int V, bool f32);       // at most 64
+ScoreTake score_take(int T, int V, int top, bool f32, int parts);
 inline size_t score_stat_bytes(int T, int parts) { return (static_cast<size_t>(T) * parts * 16 + 255) / 256 * 256; }
 
 hipError_t launch_scores(const ScoreArgs& a, bool f32, hipStream_t st);

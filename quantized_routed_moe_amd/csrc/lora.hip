@@ -2,26 +2,38 @@
 // v = a[g] x for every token with an adapter g, then out = base + scales[g] b[g] v.
 //
 // Few operations a byte: bound by HBM (x, the active adapters, base and out),
-// with few tokens by launches and latency.  Two launches.  The shrink takes
-// runs of 16 tokens of one adapter, 16 to 64 ranks and a part of K; its waves
-// split the part, and their sums meet in LDS in wave order.  The expand takes a
-// run of up to 64 tokens and 256 columns and adds the parts of v in order, so
-// nothing depends on timing.
+// with few tokens by launches and latency.
 //
-// Both are 16x16x32 bf16 products with the weights as operand A, so a lane's
-// four results are neighbouring ranks or columns of one token.  bf16 products
-// are exact in fp32.  v is fp32: for the expand it is split into three bf16
-// parts that hold its 24 bits, and three products are added (the matrix work is a
-// few per cent of the time that base and out take).
+// The shrink takes a run of up to 64 tokens of one adapter, 16 to 64 ranks and a
+// part of K; its eight waves split the part, and their sums meet in LDS in wave
+// order.  The expand takes up to 32 tokens of a run and 512 columns and adds the
+// parts of v in order, so nothing depends on timing.
+//
+// Both are 16x16x32 bf16 products, exact in fp32 but for the sums.  v is fp32: for
+// the expand it is split into three bf16 parts that hold its 24 bits, and three
+// products are added (the matrix work is a few per cent of the time that base and
+// out take).
+//
+// A load whose neighbouring lanes are in different rows moves a quarter of what
+// one does whose four lanes of a quad share 64 bytes.  So a shrink operand of 16
+// rows x 32 values is loaded as lane = (row, 16-byte chunk) and turned into the
+// instruction's (chunk, row) by a lane permutation; and the expand has tokens as
+// operand A and, as column c of fragment f, weight row 8 c + f, so that a lane's
+// eight fragments are eight neighbouring columns of its four tokens.
 #include "batch.hpp"
 
 namespace qrmoe {
 
 namespace {
 
-constexpr int kShrinkStep = 64;                // values of K a wave takes at a time: one cache line of a row
 constexpr int kShrinkWaves = 8;
-constexpr int kExpandCols = 256;
+constexpr int kExpandWaves = 4;
+constexpr int kExpandCols = 128 * kExpandWaves;
+constexpr int kHalfRows = 32, kHalves = kItemRows / kHalfRows;
+constexpr int kOneWaves = 8;
+constexpr int kOneCols = 128 * kOneWaves;
+constexpr int kMostSplits = 8;
+constexpr int kStep = 128;                     // values of K of four products
 
 struct Run {
     int g, r0, r1;
@@ -37,275 +49,727 @@ __device__ __forceinline__ Run load_run(const LoraArgs& a, int i) {
     return r;
 }
 
-// Token of entry i of perm, or -1.
-__device__ __forceinline__ int token_at(const LoraArgs& a, int i) {
-    const int t = a.perm[i];
-    return t >= 0 && t < a.T ? t : -1;
+// No load before this point is moved behind it: left to itself the compiler puts
+// each load into the branch that uses it and waits there.
+__device__ __forceinline__ void hold_loads() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
 }
 
-// RF: fragments of 16 ranks.
-template <int RF>
-__global__ __launch_bounds__(kShrinkWaves* kWave) void lora_shrink_kernel(LoraArgs a) {
-    __shared__ __align__(16) float part[kShrinkWaves][RF * 256];
-    const int sub = blockIdx.x % 4, split = blockIdx.y;
-    Run run = load_run(a, blockIdx.x / 4);
-    run.r0 += 16 * sub;
-    if (run.g < 0 || run.g == a.L || run.r0 >= run.r1) return;
-    const int rows = min(16, run.r1 - run.r0), j0 = blockIdx.z * (16 * RF);
-    const int lane = threadIdx.x & 63, g = lane >> 4, col = lane & 15;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int S = ceil_div(a.K, kShrinkStep), slice = split * kShrinkWaves + wave, slices = a.splits * kShrinkWaves;
-    const int s_beg = static_cast<long long>(S) * slice / slices, s_end = static_cast<long long>(S) * (slice + 1) / slices;
-
-    const uint16_t* arow[RF];
+// Four loads of a lane as four operands: load i holds chunk l % 4 (16 bytes) of
+// piece l / 16 of row 4 (l / 4 % 4) + i; operand i is to hold chunk i of piece
+// l / 16 of row l % 16, which is a transposition within every four lanes.
+__device__ __forceinline__ void turn(const u32x4 (&v)[4], bf16x8 (&o)[4]) {
+    const bool odd = threadIdx.x & 1, high = threadIdx.x & 2;
+    auto flip1 = [](uint32_t x) { return static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(x), 0xB1, 0xf, 0xf, true)); };
+    auto flip2 = [](uint32_t x) { return static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(x), 0x4E, 0xf, 0xf, true)); };
+    u32x4 r[4];
 #pragma unroll
-    for (int f = 0; f < RF; ++f)
-        arow[f] = a.a + (static_cast<size_t>(run.g) * a.r + min(j0 + 16 * f + col, a.r - 1)) * a.K;
-    const int t = max(token_at(a, run.r0 + min(col, rows - 1)), 0);
-    const uint16_t* xrow = a.x + t * a.x_stride;
-    f32x4 acc[RF];
+    for (int d = 0; d < 4; ++d) {
+        uint32_t a[4];
 #pragma unroll
-    for (int f = 0; f < RF; ++f) acc[f] = f32x4{0.f, 0.f, 0.f, 0.f};
-    // 16 bytes of a row from value k on, zeros past K (a multiple of 32)
-    auto chunk = [&](const uint16_t* row, int k) {
-        const u32x4 v = *reinterpret_cast<const u32x4*>(row + (k < a.K ? k : 0));
-        return bf16x8_from_u32x4(k < a.K ? v : u32x4{0u, 0u, 0u, 0u});
-    };
-#pragma unroll 2
-    for (int s = s_beg; s < s_end; ++s) {
-        const int k = s * kShrinkStep + 8 * g;
-        const bf16x8 x0 = chunk(xrow, k), x1 = chunk(xrow, k + 32);
-#pragma unroll
-        for (int f = 0; f < RF; ++f) {
-            acc[f] = mfma16x16x32(chunk(arow[f], k), x0, acc[f]);
-            acc[f] = mfma16x16x32(chunk(arow[f], k + 32), x1, acc[f]);
+        for (int i = 0; i < 4; i += 2) {
+            const uint32_t even = flip1(v[i][d]), next = flip1(v[i + 1][d]);       // by all lanes
+            a[i] = odd ? next : v[i][d];
+            a[i + 1] = odd ? v[i + 1][d] : even;
         }
-    }
-    // value [token col][rank 16 f + 4 g + i]
 #pragma unroll
-    for (int f = 0; f < RF; ++f) *reinterpret_cast<f32x4*>(&part[wave][col * 16 * RF + 16 * f + 4 * g]) = acc[f];
-    __syncthreads();
-    for (int i = threadIdx.x; i < rows * 16 * RF; i += kShrinkWaves * kWave) {
-        const int j = j0 + i % (16 * RF);
-        if (j >= a.r) continue;
-        float v = 0.f;
-#pragma unroll
-        for (int w = 0; w < kShrinkWaves; ++w) v += part[w][i];
-        a.v[(static_cast<size_t>(split) * a.T + run.r0 + i / (16 * RF)) * a.r + j] = v;
-    }
-}
-
-// Three bf16 parts of eight floats, exact to 2^-24: each subtraction is exact
-// and each part takes the next 8 bits.
-__device__ __forceinline__ void split_parts(const f32x4& lo, const f32x4& hi, bf16x8 (&p)[3]) {
-    u32x4 w[3];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        f32x2 v = i < 2 ? f32x2{lo[2 * i], lo[2 * i + 1]} : f32x2{hi[2 * i - 4], hi[2 * i - 3]};
-#pragma unroll
-        for (int q = 0; q < 3; ++q) {
-            w[q][i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
-            v = f32x2{v[0] - bf16lo(w[q][i]), v[1] - bf16hi(w[q][i])};
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t low = flip2(a[i]), next = flip2(a[i + 2]);
+            r[i][d] = high ? next : a[i];
+            r[i + 2][d] = high ? a[i + 2] : low;
         }
     }
 #pragma unroll
-    for (int q = 0; q < 3; ++q) p[q] = bf16x8_from_u32x4(w[q]);
+    for (int i = 0; i < 4; ++i) o[i] = bf16x8_from_u32x4(r[i]);
 }
 
-// Eight neighbouring values of base or out.
-template <bool F32>
-struct Eight {
-    f32x4 lo, hi;
-    __device__ __forceinline__ void load(const void* base, long long at, int n, bool vec) {
-        if constexpr (F32) {
-            const float* p = static_cast<const float*>(base) + at;
-            if (vec && n >= 8) {
-                lo = *reinterpret_cast<const f32x4*>(p);
-                hi = *reinterpret_cast<const f32x4*>(p + 4);
-            } else {
+// Sums of a wave's steps [beg, end) of K: ranks j0 + 16 f + .. times the run's
+// tokens 16 q + ..; lane l has ranks 4 (l / 16) + i of token l % 16.  AHEAD: steps
+// on their way.
+template <int RF, int TT, int AHEAD>
+struct Sums {
+    f32x4 acc[RF * TT];
+    u32x4 av[AHEAD][RF][4], xv[AHEAD][TT][4];
+    const uint16_t *arow, *xrow[TT][4];        // arow: of fragment 0 (uniform)
+    int aoff[RF];                              // the lane's place in a fragment
+
+    static __device__ __forceinline__ int lane_k() { return 8 * (threadIdx.x & 3) + 32 * (threadIdx.x >> 4 & 3); }
+
+    // Rows, and the first steps' loads.
+    __device__ __forceinline__ void begin(const LoraArgs& a, const Run& run, int j0, int beg, int end) {
+        const int row = threadIdx.x & 12;
+        int t[TT][4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    lo[i] = i < n ? p[i] : 0.f;
-                    hi[i] = 4 + i < n ? p[4 + i] : 0.f;
+        for (int q = 0; q < TT; ++q)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) t[q][i] = a.perm[min(run.r0 + 16 * q + row + i, run.r1 - 1)];
+        arow = a.a + (static_cast<size_t>(run.g) * a.r + j0) * a.K;
+#pragma unroll
+        for (int f = 0; f < RF; ++f) aoff[f] = min(16 * f + row, a.r - j0 - 4) * a.K;      // r is a multiple of 8
+        load_a(a, beg, end);
+#pragma unroll
+        for (int q = 0; q < TT; ++q)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) xrow[q][i] = a.x + (t[q][i] >= 0 && t[q][i] < a.T ? t[q][i] : 0) * a.x_stride;
+        load_x(a, beg, end);
+#pragma unroll
+        for (int i = 0; i < RF * TT; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+    // The lane's place in step s; past K (a multiple of 32) or the last step any other.
+    static __device__ __forceinline__ int place(const LoraArgs& a, int s, int end) {
+        const int k = kStep * min(s, max(end - 1, 0)) + lane_k();
+        return k < a.K ? k : lane_k() < a.K ? lane_k() : 0;
+    }
+    __device__ __forceinline__ void load_a(const LoraArgs& a, int s, int end) {
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u) {
+            const int k = place(a, s + u, end);
+#pragma unroll
+            for (int f = 0; f < RF; ++f)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) av[u][f][i] = *reinterpret_cast<const u32x4*>(arow + i * a.K + (aoff[f] + k));
+        }
+    }
+    __device__ __forceinline__ void load_x(const LoraArgs& a, int s, int end) {
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u) {
+            const int k = place(a, s + u, end);
+#pragma unroll
+            for (int q = 0; q < TT; ++q)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) xv[u][q][i] = *reinterpret_cast<const u32x4*>(xrow[q][i] + k);
+        }
+    }
+    __device__ __forceinline__ void run_steps(const LoraArgs& a, int beg, int end) {
+        for (int s = beg; s < end; s += AHEAD) {
+            hold_loads();
+#pragma unroll
+            for (int u = 0; u < AHEAD; ++u) {
+                if (s + u >= end) break;
+                if (kStep * (s + u + 1) > a.K && kStep * (s + u) + lane_k() >= a.K) {
+#pragma unroll
+                    for (int q = 0; q < TT; ++q)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) xv[u][q][i] = u32x4{0u, 0u, 0u, 0u};
+                }
+                bf16x8 ao[RF][4];
+#pragma unroll
+                for (int f = 0; f < RF; ++f) turn(av[u][f], ao[f]);
+#pragma unroll
+                for (int q = 0; q < TT; ++q) {
+                    bf16x8 xo[4];
+                    turn(xv[u][q], xo);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int f = 0; f < RF; ++f) acc[f * TT + q] = mfma16x16x32(ao[f][i], xo[i], acc[f * TT + q]);
                 }
             }
-        } else {
-            const uint16_t* p = static_cast<const uint16_t*>(base) + at;
-            u32x4 w;
-            if (vec && n >= 8) {
-                w = *reinterpret_cast<const u32x4*>(p);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    w[i] = (2 * i < n ? p[2 * i] : 0u) | (2 * i + 1 < n ? static_cast<uint32_t>(p[2 * i + 1]) << 16 : 0u);
-            }
-            lo = f32x4{bf16lo(w[0]), bf16hi(w[0]), bf16lo(w[1]), bf16hi(w[1])};
-            hi = f32x4{bf16lo(w[2]), bf16hi(w[2]), bf16lo(w[3]), bf16hi(w[3])};
-        }
-    }
-    __device__ __forceinline__ void store(void* out, long long at, int n, bool vec) const {
-        if constexpr (F32) {
-            float* p = static_cast<float*>(out) + at;
-            if (vec && n >= 8) {
-                *reinterpret_cast<f32x4*>(p) = lo;
-                *reinterpret_cast<f32x4*>(p + 4) = hi;
-            } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if (i < n) p[i] = lo[i];
-                    if (4 + i < n) p[4 + i] = hi[i];
-                }
-            }
-        } else {
-            uint16_t* p = static_cast<uint16_t*>(out) + at;
-            const float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-            if (vec && n >= 8) {
-                u32x4 w;
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    w[i] = f32_to_bf16_rne(v[2 * i]) | static_cast<uint32_t>(f32_to_bf16_rne(v[2 * i + 1])) << 16;
-                *reinterpret_cast<u32x4*>(p) = w;
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (i < n) p[i] = f32_to_bf16_rne(v[i]);
+            if (s + AHEAD < end) {
+                load_a(a, s + AHEAD, end);
+                load_x(a, s + AHEAD, end);
             }
         }
     }
 };
 
-// A wave's 64 columns from n0 on and 16 TT tokens.  Fragment f of 16 weight rows
-// holds columns 32 (f/2) + 8 (row/4) + 4 (f%2) + row%4, so the two fragments of a
-// pair give a lane eight neighbouring columns of its token.
-template <bool F32, int TT>
-__device__ __forceinline__ void expand_body(const LoraArgs& a, const Run& run, int n0) {
-    const int lane = threadIdx.x & 63, g = lane >> 4, col = lane & 15;
-    const uint16_t* brow[4];
+// The waves' sums added in wave order; put(token of the run, first of four
+// ranks, values).  Four ranks past r may come, none of them a rank below it.
+template <int WAVES, int RF, int TT, typename Put>
+__device__ __forceinline__ void shrink_join(int j0, const f32x4 (&acc)[RF * TT], f32x4* part, Put put) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
 #pragma unroll
-    for (int f = 0; f < 4; ++f) {
-        const int n = n0 + 32 * (f / 2) + 8 * (col / 4) + 4 * (f % 2) + col % 4;
-        brow[f] = a.b + (static_cast<size_t>(run.g) * a.N + min(n, a.N - 1)) * a.r;
+    for (int i = 0; i < RF * TT; ++i) part[(wave * RF * TT + i) * kWave + lane] = acc[i];
+    __syncthreads();
+    for (int i = threadIdx.x; i < RF * TT * kWave; i += WAVES * kWave) {
+        f32x4 v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) v += part[w * RF * TT * kWave + i];
+        const int l = i % kWave, f = i / kWave / TT, q = i / kWave % TT;
+        put(16 * q + l % 16, j0 + 16 * f + 4 * (l / 16), v);
     }
-    int t[TT];
-    Eight<F32> base[TT][2];
+}
+
+template <int RF, int TT>
+__device__ __forceinline__ void shrink_body(const LoraArgs& a, const Run& run, f32x4* part) {
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), split = blockIdx.y, j0 = blockIdx.z * (16 * RF);
+    const long long P = ceil_div(a.K, kStep);
+    const int slice = split * kShrinkWaves + wave, slices = a.splits * kShrinkWaves;
+    const int beg = P * slice / slices, end = P * (slice + 1) / slices;
+    Sums<RF, TT, (RF + TT <= 2 ? 2 : 1)> sums;
+    sums.begin(a, run, j0, beg, end);
+    sums.run_steps(a, beg, end);
+    float* v = a.v + static_cast<size_t>(split) * a.T * a.r;
+    shrink_join<kShrinkWaves, RF, TT>(j0, sums.acc, part, [&](int i, int j, const f32x4& s) {
+        if (run.r0 + i < run.r1 && j < a.r) *reinterpret_cast<f32x4*>(v + static_cast<size_t>(run.r0 + i) * a.r + j) = s;
+    });
+}
+
+// Up to 32 tokens of an item: the first halves of all items, then the second,
+// of which few have tokens where adapters have few: workgroups go round the XCDs,
+// and alternating halves left every second XCD idle.
+__device__ __forceinline__ Run load_half(const LoraArgs& a, int at) {
+    Run run = load_run(a, at % a.n_items);
+    run.r0 += kHalfRows * (at / a.n_items);
+    run.r1 = min(run.r1, run.r0 + kHalfRows);
+    if (run.r0 >= run.r1) run.g = -1;
+    return run;
+}
+
+// RF: fragments of 16 ranks.
+template <int RF>
+__global__ __launch_bounds__(kShrinkWaves* kWave, 4) void lora_shrink_kernel(LoraArgs a) {
+    __shared__ __align__(16) f32x4 part[kShrinkWaves * RF * 2 * kWave];
+    const Run run = load_half(a, blockIdx.x);
+    if (run.g < 0 || run.g == a.L) return;
+    if (run.r1 - run.r0 > 16) shrink_body<RF, 2>(a, run, part);
+    else shrink_body<RF, 1>(a, run, part);
+}
+
+// Two floats to bf16, nearest even, in one instruction (a NaN stays one).
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{lo, hi}, bf16x2));
+}
+
+// Three bf16 parts of four floats, exact to 2^-24: each subtraction is exact
+// and each part takes the next 8 bits.
+__device__ __forceinline__ void split_parts(const f32x4& v, u32x2 (&p)[3]) {
 #pragma unroll
-    for (int q = 0; q < TT; ++q) {
-        const int i = run.r0 + 16 * q + col;
-        t[q] = i < run.r1 ? token_at(a, i) : -1;
+    for (int i = 0; i < 2; ++i) {
+        float a = v[2 * i], b = v[2 * i + 1];
 #pragma unroll
-        for (int p = 0; p < 2; ++p) {
-            const int n = n0 + 32 * p + 8 * g;
-            if (t[q] >= 0 && n < a.N) base[q][p].load(a.base, t[q] * a.base_stride + n, a.N - n, a.vec);
+        for (int q = 0; q < 3; ++q) {
+            p[q][i] = bf16_pair(a, b);
+            a -= bf16lo(p[q][i]);
+            b -= bf16hi(p[q][i]);
         }
     }
-    f32x4 acc[4][TT];
+}
+
+// A lane's eight values of a row of base or out.  VEC: eight neighbouring
+// columns from n on, whole 16 bytes, N a multiple of 8.  Else values 16 columns apart,
+// so that neighbouring lanes have neighbouring columns.  Loads are unconditional
+// (n is clamped) and converted when they are used.
+template <bool F32, bool VEC>
+struct Eight {
+    static constexpr int step = VEC ? 1 : 16;
+    static constexpr int words = VEC ? (F32 ? 8 : 4) : 8;
+    uint32_t w[words];
+    __device__ __forceinline__ void load(const void* base, long long row, int n, int N) {
+        if constexpr (VEC) {
+            const char* p = static_cast<const char*>(base) + (row + min(n, N - 8)) * (F32 ? 4 : 2);
 #pragma unroll
-    for (int f = 0; f < 4; ++f)
+            for (int h = 0; h < words / 4; ++h) {
+                const u32x4 v = reinterpret_cast<const u32x4*>(p)[h];
 #pragma unroll
-        for (int q = 0; q < TT; ++q) acc[f][q] = f32x4{0.f, 0.f, 0.f, 0.f};
-    for (int j = 8 * g; j - 8 * g < a.r; j += 32) {
-        const bool live = j < a.r;             // r is a multiple of 8
-        bf16x8 w[4];
-#pragma unroll
-        for (int f = 0; f < 4; ++f) {
-            const u32x4 v = *reinterpret_cast<const u32x4*>(brow[f] + (live ? j : 0));
-            w[f] = bf16x8_from_u32x4(live ? v : u32x4{0u, 0u, 0u, 0u});
-        }
-#pragma unroll
-        for (int q = 0; q < TT; ++q) {
-            f32x4 lo = {0.f, 0.f, 0.f, 0.f}, hi = lo;
-            if (live) {
-                const float* v = a.v + static_cast<size_t>(min(run.r0 + 16 * q + col, run.r1 - 1)) * a.r + j;
-                for (int s = 0; s < a.splits; ++s) {
-                    const f32x4* p = reinterpret_cast<const f32x4*>(v + static_cast<size_t>(s) * a.T * a.r);
-                    lo += p[0];
-                    hi += p[1];
-                }
+                for (int i = 0; i < 4; ++i) w[4 * h + i] = v[i];
             }
-            bf16x8 parts[3];
-            split_parts(lo, hi, parts);
+        } else {
 #pragma unroll
-            for (int f = 0; f < 4; ++f)
+            for (int i = 0; i < 8; ++i) {
+                const long long at = row + min(n + step * i, N - 1);
+                w[i] = F32 ? static_cast<const uint32_t*>(base)[at] : static_cast<const uint16_t*>(base)[at];
+            }
+        }
+    }
+    __device__ __forceinline__ float value(int i) const {
+        if constexpr (F32) return __uint_as_float(w[i]);
+        else if constexpr (VEC) return i % 2 ? bf16hi(w[i / 2]) : bf16lo(w[i / 2]);
+        else return bf16lo(w[i]);
+    }
+};
+
+template <bool F32, bool VEC>
+__device__ __forceinline__ void store8(void* out, long long row, int n, int N, const float (&v)[8]) {
+    if constexpr (VEC) {
+        if (n >= N) return;
+        char* p = static_cast<char*>(out) + (row + n) * (F32 ? 4 : 2);
+        if constexpr (F32) {
+            reinterpret_cast<f32x4*>(p)[0] = f32x4{v[0], v[1], v[2], v[3]};
+            reinterpret_cast<f32x4*>(p)[1] = f32x4{v[4], v[5], v[6], v[7]};
+        } else {
+            u32x4 w;
 #pragma unroll
-                for (int p = 2; p >= 0; --p) acc[f][q] = mfma16x16x32(w[f], parts[p], acc[f][q]);
+            for (int i = 0; i < 4; ++i) w[i] = bf16_pair(v[2 * i], v[2 * i + 1]);
+            *reinterpret_cast<u32x4*>(p) = w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (n + 16 * i >= N) break;
+            if constexpr (F32) static_cast<float*>(out)[row + n + 16 * i] = v[i];
+            else static_cast<uint16_t*>(out)[row + n + 16 * i] = static_cast<uint16_t>(bf16_pair(v[i], v[i]));
+        }
+    }
+}
+
+// The tokens' v as operands: three parts of ROWS rows of ranks, a row's 32 KS
+// ranks and 16 bytes more, so that 16 rows' chunks lie in distinct banks.
+template <int ROWS, int KS>
+struct Parts {
+    static constexpr int row_bytes = 64 * KS + 16;
+    uint8_t b[3][ROWS][row_bytes];
+    // ranks j .. j + 3 of a row
+    __device__ __forceinline__ void set(int row, int j, const f32x4& v) {
+        u32x2 p[3];
+        split_parts(v, p);
+#pragma unroll
+        for (int q = 0; q < 3; ++q) *reinterpret_cast<u32x2*>(&b[q][row][2 * j]) = p[q];
+    }
+    // lane l: ranks 32 s + 8 (l / 16) + .. of row 16 q + l % 16
+    __device__ __forceinline__ bf16x8 get(int part, int q, int s) const {
+        const int lane = threadIdx.x & 63;
+        return *reinterpret_cast<const bf16x8*>(&b[part][16 * q + (lane & 15)][64 * s + 16 * (lane >> 4)]);
+    }
+};
+
+// First of a lane's eight columns in a wave's 128 from n0 on.
+template <bool VEC>
+__device__ __forceinline__ int lane_column(int n0) {
+    return n0 + (VEC ? 8 : 1) * (threadIdx.x & 15);
+}
+
+// Weights of a wave's 128 columns, ranks 32 s to 32 s + 31, on their way to
+// operands: rows of 64 bytes (or all r ranks, if fewer) are loaded as they lie,
+// whole lines, and turned round in LDS.  put(): row 8 c + f (16 f + c where not VEC) at
+// place (f, c); 16 bytes more per row and 32 per f keep the writes of neighbouring
+// rows and the reads of 16 c in distinct banks.  get(f): lane l has ranks 8 (l /
+// 16) + .. of column c = l % 16.
+template <bool VEC>
+struct Weights {
+    static constexpr int row_bytes = 80, f_bytes = 16 * row_bytes + 32;
+    u32x4 v[8];
+    // A wave's share of LDS.
+    struct Share {
+        uint8_t b[8 * f_bytes];
+    };
+    // chunks of a row in step s, and at / chunks for at < 512
+    static __device__ __forceinline__ int chunks_of(const LoraArgs& a, int s) { return min(a.r - 32 * s, 32) / 8; }
+    static __device__ __forceinline__ int row_of(int at, int chunks) {
+        return at * (chunks == 4 ? 16384 : chunks == 3 ? 21846 : chunks == 2 ? 32768 : 65536) >> 16;
+    }
+    __device__ __forceinline__ void load(const LoraArgs& a, int g, int n0, int s) {
+        const int lane = threadIdx.x & 63, chunks = chunks_of(a, s);
+        const uint16_t* from = a.b + static_cast<size_t>(g) * a.N * a.r + 32 * s;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (64 * i >= 128 * chunks) break;
+            const int at = 64 * i + lane, row = row_of(at, chunks);
+            v[i] = *reinterpret_cast<const u32x4*>(from + static_cast<size_t>(min(n0 + row, a.N - 1)) * a.r + 8 * (at - row * chunks));
+        }
+    }
+    __device__ __forceinline__ void put(const LoraArgs& a, int s, Share& to) const {
+        const int lane = threadIdx.x & 63, chunks = chunks_of(a, s);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (64 * i >= 128 * chunks) break;
+            const int at = 64 * i + lane, row = row_of(at, chunks);
+            const int f = VEC ? row % 8 : row / 16, c = VEC ? row / 8 : row % 16;
+            *reinterpret_cast<u32x4*>(to.b + f * f_bytes + c * row_bytes + 16 * (at - row * chunks)) = v[i];
+        }
+    }
+    static __device__ __forceinline__ bf16x8 get(const LoraArgs& a, int s, const Share& from, int f) {
+        const int lane = threadIdx.x & 63, j = lane >> 4;
+        // past r: any ranks, their v are zeros
+        const int chunk = 32 * s + 8 * j < a.r ? j : 0;
+        return *reinterpret_cast<const bf16x8*>(from.b + f * f_bytes + (lane & 15) * row_bytes + 16 * chunk);
+    }
+};
+
+// The lane's four tokens of a tile of 16: rows of base and out, or -1.
+struct Tokens {
+    int t[4];
+    __device__ __forceinline__ void load(const LoraArgs& a, const Run& run, int first) {
+        const int at = first + 4 * (threadIdx.x >> 4 & 3);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) t[i] = a.perm[min(at + i, a.T - 1)];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) t[i] = at + i < run.r1 && t[i] >= 0 && t[i] < a.T ? t[i] : -1;
+    }
+};
+
+template <bool F32, bool VEC>
+__device__ __forceinline__ void load_base(const LoraArgs& a, const Tokens& t, int n, Eight<F32, VEC> (&base)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) base[i].load(a.base, max(t.t[i], 0) * a.base_stride, n, a.N);
+}
+
+template <bool F32, bool VEC>
+__device__ __forceinline__ void store_sum(const LoraArgs& a, const Tokens& t, int n, float scale, const f32x4 (&acc)[8],
+                                          const Eight<F32, VEC> (&base)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (t.t[i] < 0) continue;
+        float v[8];
+#pragma unroll
+        for (int f = 0; f < 8; ++f) v[f] = fmaf(scale, acc[f][i], base[i].value(f));
+        store8<F32, VEC>(a.out, t.t[i] * a.out_stride, n, a.N, v);
+    }
+}
+
+template <int ROWS, int KS>
+__device__ __forceinline__ void add_products(const Parts<ROWS, KS>& v, const bf16x8 (&w)[8], int q, int s, f32x4 (&acc)[8]) {
+#pragma unroll
+    for (int p = 2; p >= 0; --p) {
+        const bf16x8 t = v.get(p, q, s);
+#pragma unroll
+        for (int f = 0; f < 8; ++f) acc[f] = mfma16x16x32(t, w[f], acc[f]);
+    }
+}
+
+// Rows of no adapter: base as it is, 128 columns of a wave.
+template <bool F32, bool VEC>
+__device__ __forceinline__ void copy_rows(const LoraArgs& a, const Run& run, int n0) {
+    const int n = lane_column<VEC>(n0);
+    for (int r = run.r0; r < run.r1; r += 16) {
+        Tokens t;
+        Eight<F32, VEC> base[4];
+        t.load(a, run, r);
+        load_base<F32, VEC>(a, t, n, base);
+        hold_loads();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (t.t[i] < 0) continue;
+            float v[8];
+#pragma unroll
+            for (int f = 0; f < 8; ++f) v[f] = base[i].value(f);
+            store8<F32, VEC>(a.out, t.t[i] * a.out_stride, n, a.N, v);
+        }
+    }
+}
+
+// A wave's 128 columns from n0 on of the run's tokens.  TT: tiles of 16 tokens,
+// KS: steps of 32 ranks.
+template <bool F32, bool VEC, int TT, int KS>
+struct Expand {
+    static constexpr int kHeld = KS == 2 ? 2 : 1;              // steps' weights on their way
+    Tokens t[TT];
+    Eight<F32, VEC> base[TT][4];
+    Weights<VEC> w[kHeld];
+    float scale;
+    __device__ __forceinline__ void begin(const LoraArgs& a, const Run& run, int n0) {
+#pragma unroll
+        for (int s = 0; s < kHeld; ++s)
+            if (32 * s < a.r) w[s].load(a, run.g, n0, s);
+#pragma unroll
+        for (int q = 0; q < TT; ++q) t[q].load(a, run, run.r0 + 16 * q);
+        scale = a.scales ? a.scales[run.g] : 1.f;
+#pragma unroll
+        for (int q = 0; q < TT; ++q) load_base<F32, VEC>(a, t[q], lane_column<VEC>(n0), base[q]);
+    }
+    // The first step's weights are in share (w.put), the tokens' v in parts.
+    __device__ __forceinline__ void finish(const LoraArgs& a, const Run& run, int n0, const Parts<kHalfRows, KS>& parts,
+                                           typename Weights<VEC>::Share& share) {
+        constexpr int kTogether = KS == 1 ? 1 : TT;            // tiles whose sums are held over the steps
+        const int n = lane_column<VEC>(n0);
+#pragma unroll
+        for (int q0 = 0; q0 < TT; q0 += kTogether) {
+            f32x4 acc[kTogether][8];
+#pragma unroll
+            for (int q = 0; q < kTogether; ++q)
+#pragma unroll
+                for (int f = 0; f < 8; ++f) acc[q][f] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll(KS <= 2 ? KS : 1)
+            for (int s = 0; s < KS; ++s) {
+                if (32 * s >= a.r) break;
+                // the wave's own share, in order: no barrier
+                if (s) w[s % kHeld].put(a, s, share);
+                if (KS > kHeld && 32 * (s + 1) < a.r) w[0].load(a, run.g, n0, s + 1);
+                bf16x8 wo[8];
+#pragma unroll
+                for (int f = 0; f < 8; ++f) wo[f] = Weights<VEC>::get(a, s, share, f);
+#pragma unroll
+                for (int q = 0; q < kTogether; ++q) add_products(parts, wo, q0 + q, s, acc[q]);
+            }
+#pragma unroll
+            for (int q = 0; q < kTogether; ++q) store_sum<F32, VEC>(a, t[q0 + q], n, scale, acc[q], base[q0 + q]);
+        }
+    }
+};
+
+template <bool F32, bool VEC, int TT, int KS>
+__device__ __forceinline__ void expand_body(const LoraArgs& a, const Run& run, int n0, Parts<kHalfRows, KS>& parts,
+                                            typename Weights<VEC>::Share& share) {
+    Expand<F32, VEC, TT, KS> ex;
+    ex.begin(a, run, n0);
+    // v, its parts of K added in order; zeros past the run and past r
+    for (int i = threadIdx.x; i < 16 * TT * 8 * KS; i += kExpandWaves * kWave) {
+        const int row = i / (8 * KS), j = i % (8 * KS) * 4;
+        const bool live = run.r0 + row < run.r1 && j < a.r;
+        const float* v = a.v + (live ? static_cast<size_t>(run.r0 + row) * a.r + j : 0);
+        f32x4 part[kMostSplits], sum = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int s = 0; s < kMostSplits; ++s)
+            part[s] = *reinterpret_cast<const f32x4*>(v + static_cast<size_t>(min(s, a.splits - 1)) * a.T * a.r);
+#pragma unroll
+        for (int s = 0; s < kMostSplits; ++s) sum += live && s < a.splits ? part[s] : f32x4{0.f, 0.f, 0.f, 0.f};
+        parts.set(row, j, sum);
+    }
+    ex.w[0].put(a, 0, share);
+    hold_loads();
+    __syncthreads();
+    ex.finish(a, run, n0, parts, share);
+}
+
+template <bool F32, bool VEC, int KS>
+__global__ __launch_bounds__(kExpandWaves* kWave) void lora_expand_kernel(LoraArgs a, int n_tiles) {
+    __shared__ __align__(16) Parts<kHalfRows, KS> parts;
+    __shared__ __align__(16) typename Weights<VEC>::Share shares[kExpandWaves];
+    const Run run = load_half(a, blockIdx.x / n_tiles);
+    if (run.g < 0) return;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int n0 = blockIdx.x % n_tiles * kExpandCols + 128 * wave;
+    if (run.g == a.L) {
+        if (!a.in_place && n0 < a.N) copy_rows<F32, VEC>(a, run, n0);
+        return;
+    }
+    if (run.r1 - run.r0 > 16) expand_body<F32, VEC, 2, KS>(a, run, n0, parts, shares[wave]);
+    else expand_body<F32, VEC, 1, KS>(a, run, n0, parts, shares[wave]);
+}
+
+// Up to 16 tokens of the run.
+template <bool F32, bool VEC, int RF, int KS>
+__device__ __forceinline__ void one_body(const LoraArgs& a, const Run& run, int n0, f32x4* part, Parts<kHalfRows, KS>& parts,
+                                         typename Weights<VEC>::Share& share) {
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), S = ceil_div(a.K, kStep);
+    const int beg = S * wave / kOneWaves, end = S * (wave + 1) / kOneWaves;
+    Sums<RF, 1, (RF <= 2 ? 2 : 1)> sums;
+    Expand<F32, VEC, 1, KS> ex;
+    sums.begin(a, run, 0, beg, end);
+    ex.begin(a, run, n0);
+    sums.run_steps(a, beg, end);
+    ex.w[0].put(a, 0, share);
+    shrink_join<kOneWaves, RF, 1>(0, sums.acc, part, [&](int i, int j, const f32x4& v) {
+        parts.set(i, j, j < a.r ? v : f32x4{0.f, 0.f, 0.f, 0.f});
+        if (RF == 1) parts.set(i, 16 + j, f32x4{0.f, 0.f, 0.f, 0.f});      // the step's other ranks
+    });
+    __syncthreads();
+    ex.finish(a, run, n0, parts, share);
+}
+
+// Up to four tokens without the matrix instruction, whose operands would be
+// turned round for the sake of 16 rows: loads as Sums', of which a lane takes the dot
+// products with its 8 values of each token, two values an instruction (off by at most
+// 2^-22.5 of the magnitudes, measured).  The lanes of a quad are added by lane
+// exchanges, what else a row has in LDS, in order.  Then a thread has two columns.
+template <bool F32, int RF, int NT>
+__device__ __forceinline__ void few_body(const LoraArgs& a, const Run& run, int n0, float* part, float* sums) {
+    constexpr int kRanks = 16 * RF, kAhead = RF == 1 ? 4 : RF == 2 ? 2 : 1, kCols = kOneCols / (kOneWaves * kWave);
+    using S = Sums<RF, 1, 1>;
+    const int lane = threadIdx.x & 63, row = lane & 12;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), steps = ceil_div(a.K, kStep);
+    const int beg = steps * wave / kOneWaves, end = steps * (wave + 1) / kOneWaves;
+    const uint16_t* arow = a.a + static_cast<size_t>(run.g) * a.r * a.K;
+    int aoff[RF], t[NT];
+#pragma unroll
+    for (int f = 0; f < RF; ++f) aoff[f] = min(16 * f + row, a.r - 4) * a.K;
+#pragma unroll
+    for (int q = 0; q < NT; ++q) t[q] = __builtin_amdgcn_readfirstlane(a.perm[min(run.r0 + q, run.r1 - 1)]);
+    u32x4 av[kAhead][RF][4], xv[kAhead][NT];
+    const uint16_t* xrow[NT];
+    auto load_a = [&](int s) {
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+#pragma unroll
+            for (int f = 0; f < RF; ++f)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    av[u][f][i] = *reinterpret_cast<const u32x4*>(arow + i * a.K + (aoff[f] + S::place(a, s + u, end)));
+    };
+    auto load_x = [&](int s) {
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+#pragma unroll
+            for (int q = 0; q < NT; ++q) xv[u][q] = *reinterpret_cast<const u32x4*>(xrow[q] + S::place(a, s + u, end));
+    };
+    load_a(beg);
+#pragma unroll
+    for (int q = 0; q < NT; ++q) {
+        const bool sound = run.r0 + q < run.r1 && t[q] >= 0 && t[q] < a.T;
+        t[q] = sound ? t[q] : -1;
+        xrow[q] = a.x + max(t[q], 0) * a.x_stride;
+    }
+    load_x(beg);
+    // the thread's columns: weights and base
+    u32x4 w[kCols][2 * RF];
+    uint32_t base[kCols][NT];
+#pragma unroll
+    for (int c = 0; c < kCols; ++c) {
+        const int n = min(n0 + c * kOneWaves * kWave + static_cast<int>(threadIdx.x), a.N - 1);
+        const uint16_t* b = a.b + (static_cast<size_t>(run.g) * a.N + n) * a.r;
+#pragma unroll
+        for (int h = 0; h < 2 * RF; ++h) w[c][h] = *reinterpret_cast<const u32x4*>(b + (8 * h < a.r ? 8 * h : 0));
+#pragma unroll
+        for (int q = 0; q < NT; ++q) {
+            const long long at = max(t[q], 0) * a.base_stride + n;
+            base[c][q] = F32 ? static_cast<const uint32_t*>(a.base)[at] : static_cast<const uint16_t*>(a.base)[at] << 16;
         }
     }
     const float scale = a.scales ? a.scales[run.g] : 1.f;
+    hold_loads();
+
+    f32x4 acc[RF][NT];
 #pragma unroll
-    for (int q = 0; q < TT; ++q) {
-        if (t[q] < 0) continue;
+    for (int f = 0; f < RF; ++f)
 #pragma unroll
-        for (int p = 0; p < 2; ++p) {
-            const int n = n0 + 32 * p + 8 * g;
-            if (n >= a.N) continue;
-            Eight<F32> o = base[q][p];
+        for (int q = 0; q < NT; ++q) acc[f][q] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int s = beg; s < end; s += kAhead) {
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            if (s + u >= end) break;
+            if (kStep * (s + u + 1) > a.K && kStep * (s + u) + S::lane_k() >= a.K) {
+#pragma unroll
+                for (int q = 0; q < NT; ++q) xv[u][q] = u32x4{0u, 0u, 0u, 0u};
+            }
+#pragma unroll
+            for (int f = 0; f < RF; ++f)
+#pragma unroll
+                for (int q = 0; q < NT; ++q)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int d = 0; d < 4; ++d) {
+                            const uint32_t w2 = av[u][f][i][d], x2 = xv[u][q][d];
+                            acc[f][q][i] = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, w2), __builtin_bit_cast(bf16x2, x2),
+                                                                           acc[f][q][i], false);
+                        }
+        }
+        if (s + kAhead < end) {
+            load_a(s + kAhead);
+            load_x(s + kAhead);
+            hold_loads();
+        }
+    }
+    // [wave and piece][token][rank]
+#pragma unroll
+    for (int f = 0; f < RF; ++f)
+#pragma unroll
+        for (int q = 0; q < NT; ++q) {
+            f32x4 v = acc[f][q];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                o.lo[i] = fmaf(scale, acc[2 * p][q][i], o.lo[i]);
-                o.hi[i] = fmaf(scale, acc[2 * p + 1][q][i], o.hi[i]);
+                v[i] += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v[i]), 0xB1, 0xf, 0xf, true));
+                v[i] += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v[i]), 0x4E, 0xf, 0xf, true));
             }
-            o.store(a.out, t[q] * a.out_stride + n, a.N - n, a.vec);
+            if (!(lane & 3)) *reinterpret_cast<f32x4*>(part + ((4 * wave + (lane >> 4)) * NT + q) * kRanks + 16 * f + row) = v;
+        }
+    __syncthreads();
+    if (threadIdx.x < NT * kRanks) {
+        float v = 0.f;
+#pragma unroll
+        for (int p = 0; p < 4 * kOneWaves; ++p) v += part[p * NT * kRanks + threadIdx.x];
+        sums[threadIdx.x] = static_cast<int>(threadIdx.x) % kRanks < a.r ? v : 0.f;
+    }
+    __syncthreads();
+    float o[kCols][NT];
+#pragma unroll
+    for (int c = 0; c < kCols; ++c)
+#pragma unroll
+        for (int q = 0; q < NT; ++q) o[c][q] = 0.f;
+#pragma unroll
+    for (int h = 0; h < 2 * RF; ++h) {
+        if (8 * h >= a.r) break;
+#pragma unroll
+        for (int q = 0; q < NT; ++q) {
+            const f32x4 lo = *reinterpret_cast<const f32x4*>(sums + q * kRanks + 8 * h);
+            const f32x4 hi = *reinterpret_cast<const f32x4*>(sums + q * kRanks + 8 * h + 4);
+#pragma unroll
+            for (int c = 0; c < kCols; ++c)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t b = w[c][h][i];
+                    o[c][q] = fmaf(bf16lo(b), i < 2 ? lo[2 * i] : hi[2 * i - 4], o[c][q]);
+                    o[c][q] = fmaf(bf16hi(b), i < 2 ? lo[2 * i + 1] : hi[2 * i - 3], o[c][q]);
+                }
+        }
+    }
+#pragma unroll
+    for (int c = 0; c < kCols; ++c) {
+        const int n = n0 + c * kOneWaves * kWave + threadIdx.x;
+#pragma unroll
+        for (int q = 0; q < NT; ++q) {
+            if (t[q] < 0 || n >= a.N) continue;
+            const float v = fmaf(scale, o[c][q], __uint_as_float(base[c][q]));
+            const long long at = t[q] * a.out_stride + n;
+            if constexpr (F32) static_cast<float*>(a.out)[at] = v;
+            else static_cast<uint16_t*>(a.out)[at] = static_cast<uint16_t>(bf16_pair(v, v));
         }
     }
 }
 
-// Rows of no adapter: base as it is, 64 columns of a wave.
-template <bool F32>
-__device__ __forceinline__ void copy_body(const LoraArgs& a, const Run& run, int n0) {
-    const int lane = threadIdx.x & 63, n = n0 + 8 * (lane & 7);
-    if (n >= a.N) return;
-    for (int i = run.r0 + (lane >> 3); i < run.r1; i += 8) {
-        const int t = token_at(a, i);
-        if (t < 0) continue;
-        Eight<F32> v;
-        v.load(a.base, t * a.base_stride + n, a.N - n, a.vec);
-        v.store(a.out, t * a.out_stride + n, a.N - n, a.vec);
-    }
-}
-
-template <bool F32>
-__global__ __launch_bounds__(256) void lora_expand_kernel(LoraArgs a, int n_tiles) {
-    const Run run = load_run(a, blockIdx.x / n_tiles);
+// Both in one launch: every workgroup makes its tokens' v from the whole of K,
+// then 128 columns a wave.
+template <bool F32, bool VEC, int RF>
+__global__ __launch_bounds__(kOneWaves* kWave) void lora_one_kernel(LoraArgs a, int n_tiles) {
+    // one use at a time: of the few tokens' sums, or of the waves' sums
+    __shared__ __align__(16) f32x4 part[kOneWaves * RF * kWave];
+    __shared__ __align__(16) typename Weights<VEC>::Share shares[kOneWaves];
+    __shared__ __align__(16) Parts<kHalfRows, (RF + 1) / 2> parts;
+    const Run run = load_half(a, blockIdx.x / n_tiles);
     if (run.g < 0) return;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int n0 = blockIdx.x % n_tiles * kExpandCols + 64 * wave;
-    if (n0 >= a.N) return;
+    const int n0 = blockIdx.x % n_tiles * kOneCols;
     if (run.g == a.L) {
-        if (!a.in_place) copy_body<F32>(a, run, n0);
+        if (!a.in_place && n0 + 128 * wave < a.N) copy_rows<F32, VEC>(a, run, n0 + 128 * wave);
         return;
     }
     const int rows = run.r1 - run.r0;
-    if (rows > 32) expand_body<F32, 4>(a, run, n0);
-    else if (rows > 16) expand_body<F32, 2>(a, run, n0);
-    else expand_body<F32, 1>(a, run, n0);
+    float* few = reinterpret_cast<float*>(part);               // 32 * 4 * 16 RF values at most
+    float* sums = reinterpret_cast<float*>(&parts);
+    if (rows == 1) few_body<F32, RF, 1>(a, run, n0, few, sums);
+    else if (rows == 2) few_body<F32, RF, 2>(a, run, n0, few, sums);
+    else if (RF <= 2 && rows <= 4) few_body<F32, RF <= 2 ? RF : 2, 4>(a, run, n0, few, sums);
+    else {
+        // (what the next tile writes first, nobody reads any more: the barrier
+        // before parts are written is behind all reads of the last tile's)
+        for (Run tile = run; tile.r0 < run.r1; tile.r0 += 16) {
+            tile.r1 = min(tile.r0 + 16, run.r1);
+            one_body<F32, VEC, RF>(a, tile, n0 + 128 * wave, part, parts, shares[wave]);
+        }
+    }
 }
 
 template <int RF>
 void launch_shrink(const LoraArgs& a, hipStream_t st) {
-    const dim3 grid(a.n_items * 4, a.splits, ceil_div(a.r, 16 * RF));
+    const dim3 grid(a.n_items * kHalves, a.splits, ceil_div(a.r, 16 * RF));
     lora_shrink_kernel<RF><<<grid, kShrinkWaves * kWave, 0, st>>>(a);
+}
+
+template <bool F32, bool VEC>
+hipError_t launch(const LoraArgs& a, hipStream_t st) {
+    if (a.splits == 0) {
+        const int n_tiles = ceil_div(a.N, kOneCols), blocks = a.n_items * kHalves * n_tiles;
+        if (a.r <= 16) lora_one_kernel<F32, VEC, 1><<<blocks, kOneWaves * kWave, 0, st>>>(a, n_tiles);
+        else if (a.r <= 32) lora_one_kernel<F32, VEC, 2><<<blocks, kOneWaves * kWave, 0, st>>>(a, n_tiles);
+        else lora_one_kernel<F32, VEC, 4><<<blocks, kOneWaves * kWave, 0, st>>>(a, n_tiles);
+        return hipGetLastError();
+    }
+    if (a.r <= 16) launch_shrink<1>(a, st);
+    else launch_shrink<2>(a, st);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    const int n_tiles = ceil_div(a.N, kExpandCols), blocks = a.n_items * kHalves * n_tiles;
+    if (a.r <= 32) lora_expand_kernel<F32, VEC, 1><<<blocks, kExpandWaves * kWave, 0, st>>>(a, n_tiles);
+    else if (a.r <= 64) lora_expand_kernel<F32, VEC, 2><<<blocks, kExpandWaves * kWave, 0, st>>>(a, n_tiles);
+    else lora_expand_kernel<F32, VEC, 8><<<blocks, kExpandWaves * kWave, 0, st>>>(a, n_tiles);
+    return hipGetLastError();
 }
 
 }  // namespace
 
 int lora_splits(int T, int K, int r, int L) {
-    const int groups = L < T ? L : T, steps = ceil_div(K, kShrinkStep);
-    const int runs = ceil_div(T, 16) + groups / 2;         // taking it that half of the adapters end in a partial run
+    const int groups = L < T ? L : T, steps = ceil_div(K, kStep);
+    const int runs = ceil_div(T, kHalfRows) + groups / 2;      // taking it that half of the adapters end in a partial run
+    if (r <= 64 && runs <= 40 && r <= 32) return 0;
     int s = 1;
-    while (s < 8 && runs * s * 2 <= 512 && steps >= kShrinkWaves * s * 2) s *= 2;
+    while (s < kMostSplits && runs * s * 2 <= 512 && steps >= kShrinkWaves * s * 2) s *= 2;
     return s;
 }
 
 hipError_t launch_lora_add(const LoraArgs& a, hipStream_t st) {
-    if (a.r <= 16) launch_shrink<1>(a, st);
-    else if (a.r <= 32) launch_shrink<2>(a, st);
-    else launch_shrink<4>(a, st);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    const int n_tiles = ceil_div(a.N, kExpandCols), blocks = a.n_items * n_tiles;
-    if (a.f32) lora_expand_kernel<true><<<blocks, 256, 0, st>>>(a, n_tiles);
-    else lora_expand_kernel<false><<<blocks, 256, 0, st>>>(a, n_tiles);
-    return hipGetLastError();
+    if (a.f32) return a.vec ? launch<true, true>(a, st) : launch<true, false>(a, st);
+    return a.vec ? launch<false, true>(a, st) : launch<false, false>(a, st);
 }
 
 }  // namespace qrmoe

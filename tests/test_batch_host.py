@@ -52,11 +52,12 @@ def lora(T=4, K=64, N=100, r=16, L=8, x=A, xs=64, a=A, b=A, sc=A, perm=A, items=
     (dict(xs=1 << 41), qm.MOE_ERR_SHAPE), (dict(bs=99), qm.MOE_ERR_SHAPE), (dict(os=99), qm.MOE_ERR_SHAPE), (dict(os=0), qm.MOE_ERR_SHAPE),
     (dict(bs=-100), qm.MOE_ERR_SHAPE), (dict(os=1 << 41), qm.MOE_ERR_SHAPE),
     (dict(T=1 << 22, N=1 << 20, bs=1 << 20, os=1 << 20), qm.MOE_ERR_SHAPE),            # more workgroups than a grid has
-    *[(dict([(n, None)]), qm.MOE_ERR_NULL) for n in ("x", "a", "b", "perm", "items", "base", "out", "ws")],
-    *[(dict([(n, A + 8)]), qm.MOE_ERR_ALIGN) for n in ("x", "a", "b", "items", "base", "out", "ws")],
+    *[(dict([(n, None)]), qm.MOE_ERR_NULL) for n in ("x", "a", "b", "perm", "items", "base", "out")],
+    *[(dict([(n, A + 8)]), qm.MOE_ERR_ALIGN) for n in ("x", "a", "b", "items", "base", "out")],
     *[(dict([(n, A + 2)]), qm.MOE_ERR_ALIGN) for n in ("perm", "sc")],
     (dict(ty=0), qm.MOE_ERR_FORMAT), (dict(ty=3), qm.MOE_ERR_FORMAT), (dict(out=A, os=104), qm.MOE_ERR_UNSUPPORTED),
-    (dict(out=A, bs=0), qm.MOE_ERR_UNSUPPORTED), (dict(n=4 * 16 * 4 - 1), qm.MOE_ERR_WORKSPACE),
+    (dict(out=A, bs=0), qm.MOE_ERR_UNSUPPORTED), (dict(T=10000, ws=None), qm.MOE_ERR_NULL),
+    (dict(T=10000, ws=A + 8), qm.MOE_ERR_ALIGN), (dict(T=10000, n=10000 * 16 * 4 - 1), qm.MOE_ERR_WORKSPACE),
 ])
 def test_lora_refusals(over, code):
     assert lora(**over) == code
@@ -65,7 +66,7 @@ def test_lora_refusals(over, code):
 def test_lora_of_no_tokens():
     assert lora(T=0, x=None, a=None, b=None, perm=None, items=None, base=None, out=None, ws=None, n=0) == qm.MOE_OK
     wb = qm.lib().moe_lora_add_workspace_bytes
-    assert wb(0, 64, 100, 16, 8) == 0 and wb(4, 64, 100, 12, 8) == 0 and wb(4, 64, 100, 16, 8) >= 4 * 16 * 4
+    assert wb(0, 64, 100, 16, 8) == 0 and wb(4, 64, 100, 12, 8) == 0 and wb(10000, 64, 100, 16, 8) >= 10000 * 16 * 4
 
 
 def scores(T=4, V=1000, l=A, ty=BF16, st=1000, tok=A, given=1, lp=A, ent=A, top=5, ids=A, tlp=A, ws=A, n=BIG):

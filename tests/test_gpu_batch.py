@@ -199,8 +199,7 @@ def test_lora_refusals():
         with pytest.raises(ValueError):
             qm.lora_add(**{**ok, **bad})
     wide = torch.zeros((6, 96), dtype=BF16, device="cuda")
-    for bad, code in ((dict(ws=torch.empty(16, dtype=torch.uint8, device="cuda")), qm.MOE_ERR_WORKSPACE),
-                      (dict(x=wide[:, 4:68]), qm.MOE_ERR_ALIGN), (dict(base=wide[:, 1:41]), qm.MOE_ERR_ALIGN),
+    for bad, code in ((dict(x=wide[:, 4:68]), qm.MOE_ERR_ALIGN), (dict(base=wide[:, 1:41]), qm.MOE_ERR_ALIGN),
                       (dict(base=wide[:1, :40].expand(6, 40), out=wide[:, :40]), qm.MOE_ERR_UNSUPPORTED)):
         with pytest.raises(qm.MoeError) as e:
             qm.lora_add(**{**ok, **bad})
