@@ -1000,15 +1000,20 @@ def layer_fp8(x, xq, xq_scales, experts: ExpertsFp8, k: int, *, w_router=None, b
 
 # ------------------------------------------- a batch of many requests
 
-@dataclass
 class LoraPlan:
     """A batch's tokens by adapter (moe_lora_plan): perm int32 [T], offsets
-    int32 [adapters + 2], items int32 [...][4]."""
-    T: int
-    adapters: int
-    perm: object
-    offsets: object
-    items: object
+    int32 [adapters + 2], items int32 [moe_lora_items(T, adapters)][4].  The
+    tensors are checked here, once for all the calls that take the plan."""
+
+    def __init__(self, T: int, adapters: int, perm, offsets, items):
+        i32 = (_torch().int32,)
+        dev = perm.get_device()
+        if dev < 0:
+            raise ValueError("LoraPlan takes device tensors")
+        self.T, self.adapters, self.dev = T, adapters, dev
+        self.perm, self.offsets, self.items = perm, offsets, items
+        self.perm_addr = _addr(perm, i32, (T,), dev, "perm")
+        self.items_addr = _addr(items, i32, (lib().moe_lora_items(T, adapters), 4), dev, "items")
 
 
 def lora_plan(ids, adapters: int, *, stream=None) -> LoraPlan:
@@ -1055,7 +1060,7 @@ def lora_add(base, x, a, b, plan: LoraPlan, *, scales=None, out=None, ws=None, s
         with scope:
             return lora_add(base, x, a, b, plan, scales=scales, out=out, ws=ws)
     torch = _torch()
-    bf16, i32 = (torch.bfloat16,), (torch.int32,)
+    bf16 = (torch.bfloat16,)
     T, N = shape = base.shape
     L, r, K = a.shape
     if x.dtype != torch.bfloat16 or x.shape != (T, K):
@@ -1068,9 +1073,8 @@ def lora_add(base, x, a, b, plan: LoraPlan, *, scales=None, out=None, ws=None, s
     ap = _addr(a, bf16, (L, r, K), dev, "a")
     bbp = _addr(b, bf16, (L, N, r), dev, "b")
     sp = None if scales is None else _addr(scales, (torch.float32,), (L,), dev, "scales")
-    pp = _addr(plan.perm, i32, (T,), dev, "plan.perm")
-    if plan.items.get_device() != dev:
-        raise ValueError(f"the plan is on {plan.items.device}, not on device {dev}")
+    if plan.dev != dev:
+        raise ValueError(f"the plan is on device {plan.dev}, not on device {dev}")
     if out is None:
         out = torch.empty_like(base, memory_format=torch.contiguous_format)
         op, os_ = out.data_ptr(), N
@@ -1086,7 +1090,7 @@ def lora_add(base, x, a, b, plan: LoraPlan, *, scales=None, out=None, ws=None, s
         n = ws.numel() * ws.element_size()
         if ws.get_device() != dev:
             raise ValueError(f"ws is on {ws.device}, not on device {dev}")
-    rc = lb.moe_lora_add(T, K, N, r, L, xp, xs, ap, bbp, sp, pp, plan.items.data_ptr(), bp, bs, op, os_, bt,
+    rc = lb.moe_lora_add(T, K, N, r, L, xp, xs, ap, bbp, sp, plan.perm_addr, plan.items_addr, bp, bs, op, os_, bt,
                          None if ws is None else _ptr(ws, name="ws"), n, _raw_stream(dev))
     if rc:
         raise MoeError(rc, "moe_lora_add")

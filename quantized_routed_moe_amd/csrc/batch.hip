@@ -17,7 +17,7 @@ int hip_rc(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_HIP; }
 bool known_type(int t) { return t == MOE_TYPE_BF16 || t == MOE_TYPE_F32; }
 
 constexpr int kDimLimit = 1 << 30;
-constexpr int kTokenLimit = 1 << 26;      // four workgroups of 512 threads for each of its items fit a grid
+constexpr int kTokenLimit = 1 << 26;
 constexpr int64_t kStrideLimit = int64_t{1} << 40;
 constexpr int kMostTop = 64;
 constexpr int kMostGiven = 4096;
@@ -29,9 +29,7 @@ bool lora_ok(int T, int K, int N, int r, int L) {
            r <= 256;
 }
 
-size_t lora_ws(int T, int K, int r, int L) {
-    return T ? (static_cast<size_t>(lora_splits(T, K, r, L)) * T * r * 4 + 255) / 256 * 256 : 0;
-}
+constexpr long long kMostBlocks = 1ll << 23;   // of 256 threads or 512: a grid holds fewer than 2^32
 
 bool scores_ok(int T, int V, int top) {
     return T >= 0 && T < kDimLimit && V >= 1 && V < kDimLimit && top >= 0 && top <= kMostTop && top <= V;
@@ -78,7 +76,7 @@ int moe_lora_plan(int32_t T, int32_t L, const int32_t* ids, int32_t* offsets, in
 }
 
 size_t moe_lora_add_workspace_bytes(int32_t T, int32_t K, int32_t N, int32_t r, int32_t L) {
-    return lora_ok(T, K, N, r, L) ? lora_ws(T, K, r, L) : 0;
+    return lora_ok(T, K, N, r, L) && T ? lora_ws_bytes(lora_shape(T, K, N, r, L), T, r) : 0;
 }
 
 int moe_lora_add(int32_t T, int32_t K, int32_t N, int32_t r, int32_t L, const uint16_t* x, int64_t x_stride,
@@ -96,7 +94,9 @@ int moe_lora_add(int32_t T, int32_t K, int32_t N, int32_t r, int32_t L, const ui
     if (!aligned(x, 16) || !aligned(a, 16) || !aligned(b, 16) || !aligned(base, 16) || !aligned(out, 16) ||
         !aligned(items, 16) || !aligned(perm, 4) || !aligned(scales, 4))
         return MOE_ERR_ALIGN;
-    const int rc = check_ws(ws, ws_bytes, lora_ws(T, K, r, L));
+    const LoraShape shape = lora_shape(T, K, N, r, L);
+    if (shape.blocks >= kMostBlocks) return MOE_ERR_SHAPE;
+    const int rc = check_ws(ws, ws_bytes, lora_ws_bytes(shape, T, r));
     if (rc != MOE_OK) return rc;
     LoraArgs p{};
     p.T = T;
@@ -120,9 +120,9 @@ int moe_lora_add(int32_t T, int32_t K, int32_t N, int32_t r, int32_t L, const ui
     const int per = p.f32 ? 4 : 8;
     p.vec = N % 8 == 0 && base_stride % per == 0 && out_stride % per == 0;
     p.in_place = base == out;
-    p.splits = lora_splits(T, K, r, L);
+    p.splits = shape.splits;
     p.v = static_cast<float*>(ws);
-    if (static_cast<long long>(p.n_items) * ((static_cast<long long>(N) + 255) / 256) >= (1ll << 23)) return MOE_ERR_SHAPE;
+    p.flags = reinterpret_cast<unsigned long long*>(static_cast<char*>(ws) + lora_v_bytes(shape, T, r));
     return hip_rc(launch_lora_add(p, stream));
 }
 

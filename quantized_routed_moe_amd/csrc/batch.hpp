@@ -36,6 +36,16 @@ hipError_t launch_lora_plan(const PlanArgs& a, hipStream_t st);
 
 // ---- adapters
 
+// How a call is cut into workgroups (lora.hip).
+struct LoraShape {
+    int splits;                                // parts of K; 0: few tokens, no workspace
+    long long flags;                           // workgroups that make v, one flag each
+    long long blocks;                          // all
+};
+LoraShape lora_shape(int T, int K, int N, int r, int L);
+inline size_t lora_v_bytes(const LoraShape& p, int T, int r) { return (static_cast<size_t>(p.splits) * T * r * 4 + 255) / 256 * 256; }
+inline size_t lora_ws_bytes(const LoraShape& p, int T, int r) { return lora_v_bytes(p, T, r) + (p.flags * 8 + 255) / 256 * 256; }
+
 struct LoraArgs {
     int T, K, N, r, L, n_items;
     const uint16_t* x;
@@ -49,12 +59,10 @@ struct LoraArgs {
     int f32;                                   // 1: base and out are fp32, 0: bf16
     int vec;                                   // 1: eight columns of base and out lie in whole 16 bytes, N is a multiple of 8
     int in_place;
-    int splits;                                // parts of K
+    int splits;
     float* v;                                  // [splits][T][r], by entry of perm
+    unsigned long long* flags;
 };
-
-// Parts of K that workgroups of the shrink take.
-int lora_splits(int T, int K, int r, int L);
 
 hipError_t launch_lora_add(const LoraArgs& a, hipStream_t st);
 

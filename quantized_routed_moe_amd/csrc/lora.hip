@@ -2,38 +2,43 @@
 // v = a[g] x for every token with an adapter g, then out = base + scales[g] b[g] v.
 //
 // Few operations a byte: bound by HBM (x, the active adapters, base and out),
-// with few tokens by launches and latency.
-//
-// The shrink takes a run of up to 64 tokens of one adapter, 16 to 64 ranks and a
-// part of K; its eight waves split the part, and their sums meet in LDS in wave
-// order.  The expand takes up to 32 tokens of a run and 512 columns and adds the
-// parts of v in order, so nothing depends on timing.
+// with few tokens by the launch and a chain of latencies.  One launch.  First come
+// the workgroups that make v: a run of up to 32 tokens of one adapter, up to 32
+// ranks and a part of K, which their waves split, their sums meeting in LDS in wave
+// order.  Then those of the columns: up to 32 tokens of a run x 512 columns, whose
+// weights and base are on their way while they wait for v by its flags; they add
+// its parts in order, so nothing depends on timing.  (In two launches 2048 tokens x
+// 4096 x 4096 at rank 32 took 21.2 us, in one 17; 64 tokens of 64 adapters at rank
+// 16 10.2 and 8.7.)
 //
 // Both are 16x16x32 bf16 products, exact in fp32 but for the sums.  v is fp32: for
-// the expand it is split into three bf16 parts that hold its 24 bits, and three
+// the columns it is split into three bf16 parts that hold its 24 bits, and three
 // products are added (the matrix work is a few per cent of the time that base and
 // out take).
 //
-// A load whose neighbouring lanes are in different rows moves a quarter of what
-// one does whose four lanes of a quad share 64 bytes.  So a shrink operand of 16
-// rows x 32 values is loaded as lane = (row, 16-byte chunk) and turned into the
-// instruction's (chunk, row) by a lane permutation; and the expand has tokens as
-// operand A and, as column c of fragment f, weight row 8 c + f, so that a lane's
-// eight fragments are eight neighbouring columns of its four tokens.
+// A load whose neighbouring lanes are in different rows takes 3.4 times as long as
+// one whose four lanes of a quad share 64 bytes (128 KB by one workgroup: 3.4 and
+// 1.0 us).  So x and a are loaded as lane = (row, 16-byte chunk) and turned into the
+// instruction's (chunk, row) by lane exchanges, b goes through LDS, and the product
+// of the columns has tokens as operand A and, as column c of fragment f, weight row
+// 8 c + f, so that a lane's eight fragments are eight neighbouring columns of its
+// four tokens.
+//
+// Up to four tokens: few_body.
 #include "batch.hpp"
+#include "chain.hpp"
 
 namespace qrmoe {
 
 namespace {
 
-constexpr int kShrinkWaves = 8;
-constexpr int kExpandWaves = 4;
-constexpr int kExpandCols = 128 * kExpandWaves;
+constexpr int kWaves = 4;                      // of a workgroup that makes v or columns
+constexpr int kCols = 128 * kWaves;
 constexpr int kHalfRows = 32, kHalves = kItemRows / kHalfRows;
-constexpr int kOneWaves = 8;
-constexpr int kOneCols = 128 * kOneWaves;
-constexpr int kMostSplits = 8;
 constexpr int kStep = 128;                     // values of K of four products
+constexpr int kMostSplits = 8;
+constexpr int kFewWaves = 8;
+constexpr int kFewCols = 2 * kFewWaves * kWave;
 
 struct Run {
     int g, r0, r1;
@@ -174,36 +179,34 @@ struct Sums {
     }
 };
 
-// The waves' sums added in wave order; put(token of the run, first of four
-// ranks, values).  Four ranks past r may come, none of them a rank below it.
-template <int WAVES, int RF, int TT, typename Put>
-__device__ __forceinline__ void shrink_join(int j0, const f32x4 (&acc)[RF * TT], f32x4* part, Put put) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-#pragma unroll
-    for (int i = 0; i < RF * TT; ++i) part[(wave * RF * TT + i) * kWave + lane] = acc[i];
-    __syncthreads();
-    for (int i = threadIdx.x; i < RF * TT * kWave; i += WAVES * kWave) {
-        f32x4 v = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int w = 0; w < WAVES; ++w) v += part[w * RF * TT * kWave + i];
-        const int l = i % kWave, f = i / kWave / TT, q = i / kWave % TT;
-        put(16 * q + l % 16, j0 + 16 * f + 4 * (l / 16), v);
-    }
-}
-
+// The workgroup's part `split` of K and ranks from j0 on.  The waves' sums are
+// added in wave order; v is read by other workgroups of this launch.
 template <int RF, int TT>
-__device__ __forceinline__ void shrink_body(const LoraArgs& a, const Run& run, f32x4* part) {
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), split = blockIdx.y, j0 = blockIdx.z * (16 * RF);
-    const long long P = ceil_div(a.K, kStep);
-    const int slice = split * kShrinkWaves + wave, slices = a.splits * kShrinkWaves;
-    const int beg = P * slice / slices, end = P * (slice + 1) / slices;
+__device__ __forceinline__ void make_v(const LoraArgs& a, const Run& run, int split, int j0, f32x4* part) {
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const long long steps = ceil_div(a.K, kStep);
+    const int slice = split * kWaves + wave, slices = a.splits * kWaves;
+    const int beg = steps * slice / slices, end = steps * (slice + 1) / slices;
     Sums<RF, TT, (RF + TT <= 2 ? 2 : 1)> sums;
     sums.begin(a, run, j0, beg, end);
     sums.run_steps(a, beg, end);
     float* v = a.v + static_cast<size_t>(split) * a.T * a.r;
-    shrink_join<kShrinkWaves, RF, TT>(j0, sums.acc, part, [&](int i, int j, const f32x4& s) {
-        if (run.r0 + i < run.r1 && j < a.r) *reinterpret_cast<f32x4*>(v + static_cast<size_t>(run.r0 + i) * a.r + j) = s;
-    });
+#pragma unroll
+    for (int i = 0; i < RF * TT; ++i) part[(wave * RF * TT + i) * kWave + lane] = sums.acc[i];
+    __syncthreads();
+    for (int i = threadIdx.x; i < RF * TT * kWave; i += kWaves * kWave) {
+        f32x4 s = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) s += part[w * RF * TT * kWave + i];
+        // four ranks of one token; r is a multiple of 8
+        const int l = i % kWave, row = run.r0 + 16 * (i / kWave % TT) + l % 16, j = j0 + 16 * (i / kWave / TT) + 4 * (l / 16);
+        if (row >= run.r1 || j >= a.r) continue;
+        unsigned long long* to = reinterpret_cast<unsigned long long*>(v + static_cast<size_t>(row) * a.r + j);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            __hip_atomic_store(to + h, static_cast<unsigned long long>(__float_as_uint(s[2 * h + 1])) << 32 | __float_as_uint(s[2 * h]),
+                               __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
 }
 
 // Up to 32 tokens of an item: the first halves of all items, then the second,
@@ -215,16 +218,6 @@ __device__ __forceinline__ Run load_half(const LoraArgs& a, int at) {
     run.r1 = min(run.r1, run.r0 + kHalfRows);
     if (run.r0 >= run.r1) run.g = -1;
     return run;
-}
-
-// RF: fragments of 16 ranks.
-template <int RF>
-__global__ __launch_bounds__(kShrinkWaves* kWave, 4) void lora_shrink_kernel(LoraArgs a) {
-    __shared__ __align__(16) f32x4 part[kShrinkWaves * RF * 2 * kWave];
-    const Run run = load_half(a, blockIdx.x);
-    if (run.g < 0 || run.g == a.L) return;
-    if (run.r1 - run.r0 > 16) shrink_body<RF, 2>(a, run, part);
-    else shrink_body<RF, 1>(a, run, part);
 }
 
 // Two floats to bf16, nearest even, in one instruction (a NaN stays one).
@@ -440,126 +433,141 @@ __device__ __forceinline__ void copy_rows(const LoraArgs& a, const Run& run, int
 }
 
 // A wave's 128 columns from n0 on of the run's tokens.  TT: tiles of 16 tokens,
-// KS: steps of 32 ranks.
+// KS: steps of 32 ranks.  flags: those of the n workgroups that make the tokens' v.
 template <bool F32, bool VEC, int TT, int KS>
-struct Expand {
-    static constexpr int kHeld = KS == 2 ? 2 : 1;              // steps' weights on their way
+__device__ __forceinline__ void make_columns(const LoraArgs& a, const Run& run, int n0, Parts<kHalfRows, KS>& parts,
+                                             typename Weights<VEC>::Share& share, const unsigned long long* flags, int n,
+                                             int* given_up) {
+    constexpr int kHeld = KS == 1 ? 1 : 2;     // steps' weights on their way
+    constexpr int kTogether = KS == 1 ? 1 : TT;                // tiles whose sums are held over the steps
+    const int col = lane_column<VEC>(n0);
+    Weights<VEC> w[kHeld];
     Tokens t[TT];
     Eight<F32, VEC> base[TT][4];
-    Weights<VEC> w[kHeld];
-    float scale;
-    __device__ __forceinline__ void begin(const LoraArgs& a, const Run& run, int n0) {
 #pragma unroll
-        for (int s = 0; s < kHeld; ++s)
-            if (32 * s < a.r) w[s].load(a, run.g, n0, s);
+    for (int s = 0; s < kHeld; ++s)
+        if (32 * s < a.r) w[s].load(a, run.g, n0, s);
 #pragma unroll
-        for (int q = 0; q < TT; ++q) t[q].load(a, run, run.r0 + 16 * q);
-        scale = a.scales ? a.scales[run.g] : 1.f;
+    for (int q = 0; q < TT; ++q) t[q].load(a, run, run.r0 + 16 * q);
+    const float scale = a.scales ? a.scales[run.g] : 1.f;
 #pragma unroll
-        for (int q = 0; q < TT; ++q) load_base<F32, VEC>(a, t[q], lane_column<VEC>(n0), base[q]);
+    for (int q = 0; q < TT; ++q) load_base<F32, VEC>(a, t[q], col, base[q]);
+    w[0].put(a, 0, share);
+    hold_loads();
+    if (threadIdx.x < kWave) {
+        const bool there = wait_flags(flags, n, chain_tag());
+        if (threadIdx.x == 0) *given_up = !there;
     }
-    // The first step's weights are in share (w.put), the tokens' v in parts.
-    __device__ __forceinline__ void finish(const LoraArgs& a, const Run& run, int n0, const Parts<kHalfRows, KS>& parts,
-                                           typename Weights<VEC>::Share& share) {
-        constexpr int kTogether = KS == 1 ? 1 : TT;            // tiles whose sums are held over the steps
-        const int n = lane_column<VEC>(n0);
-#pragma unroll
-        for (int q0 = 0; q0 < TT; q0 += kTogether) {
-            f32x4 acc[kTogether][8];
-#pragma unroll
-            for (int q = 0; q < kTogether; ++q)
-#pragma unroll
-                for (int f = 0; f < 8; ++f) acc[q][f] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll(KS <= 2 ? KS : 1)
-            for (int s = 0; s < KS; ++s) {
-                if (32 * s >= a.r) break;
-                // the wave's own share, in order: no barrier
-                if (s) w[s % kHeld].put(a, s, share);
-                if (KS > kHeld && 32 * (s + 1) < a.r) w[0].load(a, run.g, n0, s + 1);
-                bf16x8 wo[8];
-#pragma unroll
-                for (int f = 0; f < 8; ++f) wo[f] = Weights<VEC>::get(a, s, share, f);
-#pragma unroll
-                for (int q = 0; q < kTogether; ++q) add_products(parts, wo, q0 + q, s, acc[q]);
-            }
-#pragma unroll
-            for (int q = 0; q < kTogether; ++q) store_sum<F32, VEC>(a, t[q0 + q], n, scale, acc[q], base[q0 + q]);
-        }
-    }
-};
-
-template <bool F32, bool VEC, int TT, int KS>
-__device__ __forceinline__ void expand_body(const LoraArgs& a, const Run& run, int n0, Parts<kHalfRows, KS>& parts,
-                                            typename Weights<VEC>::Share& share) {
-    Expand<F32, VEC, TT, KS> ex;
-    ex.begin(a, run, n0);
+    __syncthreads();
+    const float from = *given_up ? NAN : 0.f;
     // v, its parts of K added in order; zeros past the run and past r
-    for (int i = threadIdx.x; i < 16 * TT * 8 * KS; i += kExpandWaves * kWave) {
+    for (int i = threadIdx.x; i < 16 * TT * 8 * KS; i += kWaves * kWave) {
         const int row = i / (8 * KS), j = i % (8 * KS) * 4;
         const bool live = run.r0 + row < run.r1 && j < a.r;
         const float* v = a.v + (live ? static_cast<size_t>(run.r0 + row) * a.r + j : 0);
-        f32x4 part[kMostSplits], sum = {0.f, 0.f, 0.f, 0.f};
+        unsigned long long part[kMostSplits][2];
 #pragma unroll
-        for (int s = 0; s < kMostSplits; ++s)
-            part[s] = *reinterpret_cast<const f32x4*>(v + static_cast<size_t>(min(s, a.splits - 1)) * a.T * a.r);
+        for (int s = 0; s < kMostSplits; ++s) {
+            if (s >= a.splits) break;
+            const unsigned long long* p = reinterpret_cast<const unsigned long long*>(v + static_cast<size_t>(s) * a.T * a.r);
 #pragma unroll
-        for (int s = 0; s < kMostSplits; ++s) sum += live && s < a.splits ? part[s] : f32x4{0.f, 0.f, 0.f, 0.f};
-        parts.set(row, j, sum);
+            for (int h = 0; h < 2; ++h) part[s][h] = __hip_atomic_load(p + h, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
+        f32x4 sum = {from, from, from, from};
+#pragma unroll
+        for (int s = 0; s < kMostSplits; ++s) {
+            if (s >= a.splits) break;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                sum[2 * h] += __uint_as_float(static_cast<uint32_t>(part[s][h]));
+                sum[2 * h + 1] += __uint_as_float(static_cast<uint32_t>(part[s][h] >> 32));
+            }
+        }
+        parts.set(row, j, live ? sum : f32x4{0.f, 0.f, 0.f, 0.f});
     }
-    ex.w[0].put(a, 0, share);
-    hold_loads();
     __syncthreads();
-    ex.finish(a, run, n0, parts, share);
+#pragma unroll
+    for (int q0 = 0; q0 < TT; q0 += kTogether) {
+        f32x4 acc[kTogether][8];
+#pragma unroll
+        for (int q = 0; q < kTogether; ++q)
+#pragma unroll
+            for (int f = 0; f < 8; ++f) acc[q][f] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll kHeld
+        for (int s = 0; s < KS; ++s) {
+            if (32 * s >= a.r) break;
+            // the wave's own share, in order: no barrier
+            if (s) w[s % kHeld].put(a, s, share);
+            if (KS > kHeld && 32 * (s + kHeld) < a.r) w[s % kHeld].load(a, run.g, n0, s + kHeld);
+            bf16x8 wo[8];
+#pragma unroll
+            for (int f = 0; f < 8; ++f) wo[f] = Weights<VEC>::get(a, s, share, f);
+#pragma unroll
+            for (int q = 0; q < kTogether; ++q) add_products(parts, wo, q0 + q, s, acc[q]);
+        }
+#pragma unroll
+        for (int q = 0; q < kTogether; ++q) store_sum<F32, VEC>(a, t[q0 + q], col, scale, acc[q], base[q0 + q]);
+    }
 }
 
+// The grid: `ranks` blocks of 32 ranks x a.splits parts of K of every half item,
+// then n_tiles tiles of columns of every half item.
 template <bool F32, bool VEC, int KS>
-__global__ __launch_bounds__(kExpandWaves* kWave) void lora_expand_kernel(LoraArgs a, int n_tiles) {
-    __shared__ __align__(16) Parts<kHalfRows, KS> parts;
-    __shared__ __align__(16) typename Weights<VEC>::Share shares[kExpandWaves];
-    const Run run = load_half(a, blockIdx.x / n_tiles);
+__global__ __launch_bounds__(kWaves* kWave, KS == 1 ? 3 : KS <= 4 ? 2 : 1) void lora_kernel(LoraArgs a, int n_tiles, int ranks) {
+    struct Columns {
+        Parts<kHalfRows, KS> parts;
+        typename Weights<VEC>::Share shares[kWaves];
+        int given_up;
+    };
+    constexpr size_t kPartBytes = kWaves * 4 * kWave * sizeof(f32x4);
+    __shared__ __align__(16) uint8_t lds[sizeof(Columns) > kPartBytes ? sizeof(Columns) : kPartBytes];
+    const int each = a.splits * ranks, makers = a.n_items * kHalves * each;
+    int at = blockIdx.x;
+    if (at < makers) {
+        const Run run = load_half(a, at / each);
+        if (run.g < 0 || run.g == a.L) return;
+        f32x4* part = reinterpret_cast<f32x4*>(lds);
+        const int split = at % each / ranks, j0 = at % ranks * 32, rows = run.r1 - run.r0;
+        if (a.r <= 16) {
+            if (rows > 16) make_v<1, 2>(a, run, split, j0, part);
+            else make_v<1, 1>(a, run, split, j0, part);
+        } else {
+            if (rows > 16) make_v<2, 2>(a, run, split, j0, part);
+            else make_v<2, 1>(a, run, split, j0, part);
+        }
+        raise_flag(a.flags + at, chain_tag());
+        return;
+    }
+    at -= makers;
+    const int half = at / n_tiles;
+    const Run run = load_half(a, half);
     if (run.g < 0) return;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int n0 = blockIdx.x % n_tiles * kExpandCols + 128 * wave;
+    const int n0 = at % n_tiles * kCols + 128 * wave;
     if (run.g == a.L) {
         if (!a.in_place && n0 < a.N) copy_rows<F32, VEC>(a, run, n0);
         return;
     }
-    if (run.r1 - run.r0 > 16) expand_body<F32, VEC, 2, KS>(a, run, n0, parts, shares[wave]);
-    else expand_body<F32, VEC, 1, KS>(a, run, n0, parts, shares[wave]);
+    Columns& x = *reinterpret_cast<Columns*>(lds);
+    const unsigned long long* flags = a.flags + static_cast<size_t>(half) * each;
+    if (run.r1 - run.r0 > 16) make_columns<F32, VEC, 2, KS>(a, run, n0, x.parts, x.shares[wave], flags, each, &x.given_up);
+    else make_columns<F32, VEC, 1, KS>(a, run, n0, x.parts, x.shares[wave], flags, each, &x.given_up);
 }
 
-// Up to 16 tokens of the run.
-template <bool F32, bool VEC, int RF, int KS>
-__device__ __forceinline__ void one_body(const LoraArgs& a, const Run& run, int n0, f32x4* part, Parts<kHalfRows, KS>& parts,
-                                         typename Weights<VEC>::Share& share) {
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), S = ceil_div(a.K, kStep);
-    const int beg = S * wave / kOneWaves, end = S * (wave + 1) / kOneWaves;
-    Sums<RF, 1, (RF <= 2 ? 2 : 1)> sums;
-    Expand<F32, VEC, 1, KS> ex;
-    sums.begin(a, run, 0, beg, end);
-    ex.begin(a, run, n0);
-    sums.run_steps(a, beg, end);
-    ex.w[0].put(a, 0, share);
-    shrink_join<kOneWaves, RF, 1>(0, sums.acc, part, [&](int i, int j, const f32x4& v) {
-        parts.set(i, j, j < a.r ? v : f32x4{0.f, 0.f, 0.f, 0.f});
-        if (RF == 1) parts.set(i, 16 + j, f32x4{0.f, 0.f, 0.f, 0.f});      // the step's other ranks
-    });
-    __syncthreads();
-    ex.finish(a, run, n0, parts, share);
-}
-
-// Up to four tokens without the matrix instruction, whose operands would be
-// turned round for the sake of 16 rows: loads as Sums', of which a lane takes the dot
-// products with its 8 values of each token, two values an instruction (off by at most
-// 2^-22.5 of the magnitudes, measured).  The lanes of a quad are added by lane
-// exchanges, what else a row has in LDS, in order.  Then a thread has two columns.
+// Up to four tokens, every workgroup with the whole of their v (4096 x 4096 at
+// rank 16, us: one token 4.5, of which a launch of any size is 2.7, with v handed over
+// 6.3).  No matrix instruction, whose operands would be turned round for the sake of
+// 16 rows: loads as Sums', of which a lane takes the dot products with its 8 values of
+// each token, two values an instruction (off by at most 2^-22.5 of the magnitudes,
+// measured).  The lanes of a quad are added by lane exchanges, what else a row has in
+// LDS, in order.  Then a thread has two columns.
 template <bool F32, int RF, int NT>
 __device__ __forceinline__ void few_body(const LoraArgs& a, const Run& run, int n0, float* part, float* sums) {
-    constexpr int kRanks = 16 * RF, kAhead = RF == 1 ? 4 : RF == 2 ? 2 : 1, kCols = kOneCols / (kOneWaves * kWave);
+    constexpr int kRanks = 16 * RF, kAhead = RF == 1 ? 4 : 2, kEach = kFewCols / (kFewWaves * kWave);
     using S = Sums<RF, 1, 1>;
     const int lane = threadIdx.x & 63, row = lane & 12;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), steps = ceil_div(a.K, kStep);
-    const int beg = steps * wave / kOneWaves, end = steps * (wave + 1) / kOneWaves;
+    const int beg = steps * wave / kFewWaves, end = steps * (wave + 1) / kFewWaves;
     const uint16_t* arow = a.a + static_cast<size_t>(run.g) * a.r * a.K;
     int aoff[RF], t[NT];
 #pragma unroll
@@ -592,11 +600,11 @@ __device__ __forceinline__ void few_body(const LoraArgs& a, const Run& run, int 
     }
     load_x(beg);
     // the thread's columns: weights and base
-    u32x4 w[kCols][2 * RF];
-    uint32_t base[kCols][NT];
+    u32x4 w[kEach][2 * RF];
+    uint32_t base[kEach][NT];
 #pragma unroll
-    for (int c = 0; c < kCols; ++c) {
-        const int n = min(n0 + c * kOneWaves * kWave + static_cast<int>(threadIdx.x), a.N - 1);
+    for (int c = 0; c < kEach; ++c) {
+        const int n = min(n0 + c * kFewWaves * kWave + static_cast<int>(threadIdx.x), a.N - 1);
         const uint16_t* b = a.b + (static_cast<size_t>(run.g) * a.N + n) * a.r;
 #pragma unroll
         for (int h = 0; h < 2 * RF; ++h) w[c][h] = *reinterpret_cast<const u32x4*>(b + (8 * h < a.r ? 8 * h : 0));
@@ -658,13 +666,13 @@ __device__ __forceinline__ void few_body(const LoraArgs& a, const Run& run, int 
     if (threadIdx.x < NT * kRanks) {
         float v = 0.f;
 #pragma unroll
-        for (int p = 0; p < 4 * kOneWaves; ++p) v += part[p * NT * kRanks + threadIdx.x];
+        for (int p = 0; p < 4 * kFewWaves; ++p) v += part[p * NT * kRanks + threadIdx.x];
         sums[threadIdx.x] = static_cast<int>(threadIdx.x) % kRanks < a.r ? v : 0.f;
     }
     __syncthreads();
-    float o[kCols][NT];
+    float o[kEach][NT];
 #pragma unroll
-    for (int c = 0; c < kCols; ++c)
+    for (int c = 0; c < kEach; ++c)
 #pragma unroll
         for (int q = 0; q < NT; ++q) o[c][q] = 0.f;
 #pragma unroll
@@ -675,7 +683,7 @@ __device__ __forceinline__ void few_body(const LoraArgs& a, const Run& run, int 
             const f32x4 lo = *reinterpret_cast<const f32x4*>(sums + q * kRanks + 8 * h);
             const f32x4 hi = *reinterpret_cast<const f32x4*>(sums + q * kRanks + 8 * h + 4);
 #pragma unroll
-            for (int c = 0; c < kCols; ++c)
+            for (int c = 0; c < kEach; ++c)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const uint32_t b = w[c][h][i];
@@ -685,8 +693,8 @@ __device__ __forceinline__ void few_body(const LoraArgs& a, const Run& run, int 
         }
     }
 #pragma unroll
-    for (int c = 0; c < kCols; ++c) {
-        const int n = n0 + c * kOneWaves * kWave + threadIdx.x;
+    for (int c = 0; c < kEach; ++c) {
+        const int n = n0 + c * kFewWaves * kWave + threadIdx.x;
 #pragma unroll
         for (int q = 0; q < NT; ++q) {
             if (t[q] < 0 || n >= a.N) continue;
@@ -698,76 +706,67 @@ __device__ __forceinline__ void few_body(const LoraArgs& a, const Run& run, int 
     }
 }
 
-// Both in one launch: every workgroup makes its tokens' v from the whole of K,
-// then 128 columns a wave.
-template <bool F32, bool VEC, int RF>
-__global__ __launch_bounds__(kOneWaves* kWave) void lora_one_kernel(LoraArgs a, int n_tiles) {
-    // one use at a time: of the few tokens' sums, or of the waves' sums
-    __shared__ __align__(16) f32x4 part[kOneWaves * RF * kWave];
-    __shared__ __align__(16) typename Weights<VEC>::Share shares[kOneWaves];
-    __shared__ __align__(16) Parts<kHalfRows, (RF + 1) / 2> parts;
-    const Run run = load_half(a, blockIdx.x / n_tiles);
+template <bool F32, int RF>
+__global__ __launch_bounds__(kFewWaves* kWave) void lora_few_kernel(LoraArgs a, int n_tiles) {
+    __shared__ __align__(16) float part[4 * kFewWaves * 4 * 16 * RF];
+    __shared__ __align__(16) float sums[4 * 16 * RF];
+    Run run = load_run(a, blockIdx.x / n_tiles);
     if (run.g < 0) return;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int n0 = blockIdx.x % n_tiles * kOneCols;
+    const int n0 = blockIdx.x % n_tiles * kFewCols;
     if (run.g == a.L) {
-        if (!a.in_place && n0 + 128 * wave < a.N) copy_rows<F32, VEC>(a, run, n0 + 128 * wave);
+        if (!a.in_place) {
+            const int wave = threadIdx.x >> 6;
+            copy_rows<F32, false>(a, run, n0 + 128 * wave);
+        }
         return;
     }
-    const int rows = run.r1 - run.r0;
-    float* few = reinterpret_cast<float*>(part);               // 32 * 4 * 16 RF values at most
-    float* sums = reinterpret_cast<float*>(&parts);
-    if (rows == 1) few_body<F32, RF, 1>(a, run, n0, few, sums);
-    else if (rows == 2) few_body<F32, RF, 2>(a, run, n0, few, sums);
-    else if (RF <= 2 && rows <= 4) few_body<F32, RF <= 2 ? RF : 2, 4>(a, run, n0, few, sums);
-    else {
-        // (what the next tile writes first, nobody reads any more: the barrier
-        // before parts are written is behind all reads of the last tile's)
-        for (Run tile = run; tile.r0 < run.r1; tile.r0 += 16) {
-            tile.r1 = min(tile.r0 + 16, run.r1);
-            one_body<F32, VEC, RF>(a, tile, n0 + 128 * wave, part, parts, shares[wave]);
-        }
-    }
+    const int rows = run.r1 - run.r0;          // at most a.T
+    if (rows == 1) few_body<F32, RF, 1>(a, run, n0, part, sums);
+    else if (rows == 2) few_body<F32, RF, 2>(a, run, n0, part, sums);
+    else few_body<F32, RF, 4>(a, run, n0, part, sums);
 }
 
-template <int RF>
-void launch_shrink(const LoraArgs& a, hipStream_t st) {
-    const dim3 grid(a.n_items * kHalves, a.splits, ceil_div(a.r, 16 * RF));
-    lora_shrink_kernel<RF><<<grid, kShrinkWaves * kWave, 0, st>>>(a);
+template <bool F32>
+hipError_t launch_few(const LoraArgs& a, hipStream_t st) {
+    const int n_tiles = ceil_div(a.N, kFewCols), blocks = a.n_items * n_tiles;
+    if (a.r <= 16) lora_few_kernel<F32, 1><<<blocks, kFewWaves * kWave, 0, st>>>(a, n_tiles);
+    else lora_few_kernel<F32, 2><<<blocks, kFewWaves * kWave, 0, st>>>(a, n_tiles);
+    return hipGetLastError();
 }
 
 template <bool F32, bool VEC>
 hipError_t launch(const LoraArgs& a, hipStream_t st) {
-    if (a.splits == 0) {
-        const int n_tiles = ceil_div(a.N, kOneCols), blocks = a.n_items * kHalves * n_tiles;
-        if (a.r <= 16) lora_one_kernel<F32, VEC, 1><<<blocks, kOneWaves * kWave, 0, st>>>(a, n_tiles);
-        else if (a.r <= 32) lora_one_kernel<F32, VEC, 2><<<blocks, kOneWaves * kWave, 0, st>>>(a, n_tiles);
-        else lora_one_kernel<F32, VEC, 4><<<blocks, kOneWaves * kWave, 0, st>>>(a, n_tiles);
-        return hipGetLastError();
-    }
-    if (a.r <= 16) launch_shrink<1>(a, st);
-    else launch_shrink<2>(a, st);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    const int n_tiles = ceil_div(a.N, kExpandCols), blocks = a.n_items * kHalves * n_tiles;
-    if (a.r <= 32) lora_expand_kernel<F32, VEC, 1><<<blocks, kExpandWaves * kWave, 0, st>>>(a, n_tiles);
-    else if (a.r <= 64) lora_expand_kernel<F32, VEC, 2><<<blocks, kExpandWaves * kWave, 0, st>>>(a, n_tiles);
-    else lora_expand_kernel<F32, VEC, 8><<<blocks, kExpandWaves * kWave, 0, st>>>(a, n_tiles);
+    const int n_tiles = ceil_div(a.N, kCols), ranks = ceil_div(a.r, 32), halves = a.n_items * kHalves;
+    const int blocks = halves * (a.splits * ranks + n_tiles);
+    if (a.r <= 32) lora_kernel<F32, VEC, 1><<<blocks, kWaves * kWave, 0, st>>>(a, n_tiles, ranks);
+    else if (a.r <= 64) lora_kernel<F32, VEC, 2><<<blocks, kWaves * kWave, 0, st>>>(a, n_tiles, ranks);
+    else if (a.r <= 128) lora_kernel<F32, VEC, 4><<<blocks, kWaves * kWave, 0, st>>>(a, n_tiles, ranks);
+    else lora_kernel<F32, VEC, 8><<<blocks, kWaves * kWave, 0, st>>>(a, n_tiles, ranks);
     return hipGetLastError();
 }
 
 }  // namespace
 
-int lora_splits(int T, int K, int r, int L) {
-    const int groups = L < T ? L : T, steps = ceil_div(K, kStep);
+// Few tokens: see few_body (us: four tokens of one adapter at rank 16 6.6, else
+// 6.9; one at rank 32 6.2, 6.3; four 9.2, 6.7; one at rank 64 11.0, 7.7).  Else parts of K until the workgroups that make v are about one and a
+// half a CU (us, twice and four times as many, 4096 x 4096: 512 tokens of 64 adapters at
+// rank 64 17.4 -> 19.8 -> 22.4, 2048 tokens of 8 requests at rank 64 25.2 -> 26.2 ->
+// 31.8, at rank 16 16.8 -> 16.2 -> 16.3), with a step or more for each wave.
+LoraShape lora_shape(int T, int K, int N, int r, int L) {
+    LoraShape p{0, 0, 0};
+    if (r <= 32 && T * ceil_div(r, 16) <= 4) return p;
+    const int groups = L < T ? L : T, steps = ceil_div(K, kStep), ranks = ceil_div(r, 32);
     const int runs = ceil_div(T, kHalfRows) + groups / 2;      // taking it that half of the adapters end in a partial run
-    if (r <= 64 && runs <= 40 && r <= 32) return 0;
-    int s = 1;
-    while (s < kMostSplits && runs * s * 2 <= 512 && steps >= kShrinkWaves * s * 2) s *= 2;
-    return s;
+    p.splits = 1;
+    while (p.splits < kMostSplits && 2ll * p.splits * runs * ranks <= 380 && steps >= 2 * p.splits * kWaves) p.splits *= 2;
+    const long long halves = static_cast<long long>(plan_items(T, L)) * kHalves;
+    p.flags = halves * p.splits * ranks;
+    p.blocks = p.flags + halves * ((static_cast<long long>(N) + kCols - 1) / kCols);
+    return p;
 }
 
 hipError_t launch_lora_add(const LoraArgs& a, hipStream_t st) {
+    if (!a.splits) return a.f32 ? launch_few<true>(a, st) : launch_few<false>(a, st);
     if (a.f32) return a.vec ? launch<true, true>(a, st) : launch<true, false>(a, st);
     return a.vec ? launch<false, true>(a, st) : launch<false, false>(a, st);
 }

@@ -117,6 +117,7 @@ template <int WAVES, int ROUNDS>
 __global__ __launch_bounds__(WAVES* kWave) void plan_kernel(PlanArgs a, int bits) {
     __shared__ int cnt[WAVES * kMostGroups];   // [WAVES][G], then each wave's first place in the group
     __shared__ int start[kMostGroups + 1], first_item[kMostGroups], part[WAVES];
+    __shared__ int sorted[WAVES * ROUNDS * kWave];             // perm, from where it is written in order
     const int G = a.L + 1, wave = threadIdx.x >> 6;
     for (int i = threadIdx.x; i < WAVES * G; i += WAVES * kWave) cnt[i] = 0;
     __syncthreads();
@@ -142,10 +143,12 @@ __global__ __launch_bounds__(WAVES* kWave) void plan_kernel(PlanArgs a, int bits
         const int g = group[j];
         if (g < 0) continue;
         const int in_group = cnt[wave * G + g] + rank[j], at = start[g] + in_group;
-        a.perm[at] = t0 + 64 * j + (threadIdx.x & 63);
+        sorted[at] = t0 + 64 * j + (threadIdx.x & 63);
         if (in_group % kItemRows == 0)
             store_item(a, first_item[g] + in_group / kItemRows, g, at, min(at + kItemRows, start[g + 1]));
     }
+    __syncthreads();
+    for (int i = threadIdx.x; i < a.T; i += WAVES * kWave) a.perm[i] = sorted[i];
 }
 
 constexpr int kBlockWaves = 16, kBlockRounds = kPlanBlock / (kBlockWaves * kWave);
