@@ -1035,7 +1035,6 @@ def lora_plan(ids, adapters: int, *, stream=None) -> LoraPlan:
     # one allocation: items first, for their alignment
     new = ids.new_empty if T else ids.new_zeros
     buf = new(4 * n + T + adapters + 2)
-    perm, offsets = buf[4 * n:4 * n + T], buf[4 * n + T:]
     nw = L.moe_lora_plan_workspace_bytes(T, adapters)
     ws = ids.new_empty(nw // 4) if nw else None
     p = buf.data_ptr()
@@ -1043,7 +1042,10 @@ def lora_plan(ids, adapters: int, *, stream=None) -> LoraPlan:
                          _raw_stream(dev))
     if rc:
         raise MoeError(rc, "moe_lora_plan")
-    return LoraPlan(T, adapters, perm, offsets, buf[:4 * n].view(n, 4))
+    plan = LoraPlan.__new__(LoraPlan)          # what __init__ checks is so
+    items, plan.perm, plan.offsets = buf.split((4 * n, T, adapters + 2))
+    plan.T, plan.adapters, plan.dev, plan.items, plan.perm_addr, plan.items_addr = T, adapters, dev, items.view(n, 4), p + 16 * n, p
+    return plan
 
 
 def lora_add(base, x, a, b, plan: LoraPlan, *, scales=None, out=None, ws=None, stream=None):

@@ -8,8 +8,8 @@
 // order.  Then those of the columns: up to 32 tokens of a run x 512 columns, whose
 // weights and base are on their way while they wait for v by its flags; they add
 // its parts in order, so nothing depends on timing.  (In two launches 2048 tokens x
-// 4096 x 4096 at rank 32 took 21.2 us, in one 17; 64 tokens of 64 adapters at rank
-// 16 10.2 and 8.7.)
+// 4096 x 4096 at rank 32 took 21.2 us, in one 16.9; 64 tokens of 64 adapters at rank
+// 16 10.2 and 8.6.)
 //
 // Both are 16x16x32 bf16 products, exact in fp32 but for the sums.  v is fp32: for
 // the columns it is split into three bf16 parts that hold its 24 bits, and three
@@ -112,12 +112,16 @@ struct Sums {
         arow = a.a + (static_cast<size_t>(run.g) * a.r + j0) * a.K;
 #pragma unroll
         for (int f = 0; f < RF; ++f) aoff[f] = min(16 * f + row, a.r - j0 - 4) * a.K;      // r is a multiple of 8
-        load_a(a, beg, end);
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u) load_a(a, u, beg + u, end);
 #pragma unroll
         for (int q = 0; q < TT; ++q)
 #pragma unroll
             for (int i = 0; i < 4; ++i) xrow[q][i] = a.x + (t[q][i] >= 0 && t[q][i] < a.T ? t[q][i] : 0) * a.x_stride;
-        load_x(a, beg, end);
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u)
+#pragma unroll
+            for (int q = 0; q < TT; ++q) load_x(a, u, q, beg + u, end);
 #pragma unroll
         for (int i = 0; i < RF * TT; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
@@ -126,58 +130,79 @@ struct Sums {
         const int k = kStep * min(s, max(end - 1, 0)) + lane_k();
         return k < a.K ? k : lane_k() < a.K ? lane_k() : 0;
     }
-    __device__ __forceinline__ void load_a(const LoraArgs& a, int s, int end) {
+    __device__ __forceinline__ void load_a(const LoraArgs& a, int u, int s, int end) {
+        const int k = place(a, s, end);
 #pragma unroll
-        for (int u = 0; u < AHEAD; ++u) {
-            const int k = place(a, s + u, end);
+        for (int f = 0; f < RF; ++f)
 #pragma unroll
-            for (int f = 0; f < RF; ++f)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) av[u][f][i] = *reinterpret_cast<const u32x4*>(arow + i * a.K + (aoff[f] + k));
-        }
+            for (int i = 0; i < 4; ++i) av[u][f][i] = *reinterpret_cast<const u32x4*>(arow + i * a.K + (aoff[f] + k));
     }
-    __device__ __forceinline__ void load_x(const LoraArgs& a, int s, int end) {
+    __device__ __forceinline__ void load_x(const LoraArgs& a, int u, int q, int s, int end) {
+        const int k = place(a, s, end);
 #pragma unroll
-        for (int u = 0; u < AHEAD; ++u) {
-            const int k = place(a, s + u, end);
+        for (int i = 0; i < 4; ++i) xv[u][q][i] = *reinterpret_cast<const u32x4*>(xrow[q][i] + k);
+    }
+    // Step s, held in slot u; NEXT: each operand's place is asked to hold step s + AHEAD
+    // as soon as it is free.
+    template <bool NEXT>
+    __device__ __forceinline__ void step(const LoraArgs& a, int u, int s, int end) {
+        if (kStep * (s + 1) > a.K && kStep * s + lane_k() >= a.K) {
 #pragma unroll
             for (int q = 0; q < TT; ++q)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) xv[u][q][i] = *reinterpret_cast<const u32x4*>(xrow[q][i] + k);
+                for (int i = 0; i < 4; ++i) xv[u][q][i] = u32x4{0u, 0u, 0u, 0u};
+        }
+        bf16x8 ao[RF][4];
+#pragma unroll
+        for (int f = 0; f < RF; ++f) turn(av[u][f], ao[f]);
+        if constexpr (NEXT) {
+            load_a(a, u, s + AHEAD, end);
+            hold_loads();
+        }
+#pragma unroll
+        for (int q = 0; q < TT; ++q) {
+            bf16x8 xo[4];
+            turn(xv[u][q], xo);
+            if constexpr (NEXT) {
+                load_x(a, u, q, s + AHEAD, end);
+                hold_loads();
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int f = 0; f < RF; ++f) acc[f * TT + q] = mfma16x16x32(ao[f][i], xo[i], acc[f * TT + q]);
         }
     }
     __device__ __forceinline__ void run_steps(const LoraArgs& a, int beg, int end) {
-        for (int s = beg; s < end; s += AHEAD) {
-            hold_loads();
+        hold_loads();
+        int s = beg;
+        for (; s + 2 * AHEAD <= end; s += AHEAD)
+#pragma unroll
+            for (int u = 0; u < AHEAD; ++u) step<true>(a, u, s + u, end);
+        for (; s < end; s += AHEAD) {
 #pragma unroll
             for (int u = 0; u < AHEAD; ++u) {
                 if (s + u >= end) break;
-                if (kStep * (s + u + 1) > a.K && kStep * (s + u) + lane_k() >= a.K) {
-#pragma unroll
-                    for (int q = 0; q < TT; ++q)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) xv[u][q][i] = u32x4{0u, 0u, 0u, 0u};
-                }
-                bf16x8 ao[RF][4];
-#pragma unroll
-                for (int f = 0; f < RF; ++f) turn(av[u][f], ao[f]);
-#pragma unroll
-                for (int q = 0; q < TT; ++q) {
-                    bf16x8 xo[4];
-                    turn(xv[u][q], xo);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-#pragma unroll
-                        for (int f = 0; f < RF; ++f) acc[f * TT + q] = mfma16x16x32(ao[f][i], xo[i], acc[f * TT + q]);
-                }
+                step<false>(a, u, s + u, end);
             }
-            if (s + AHEAD < end) {
-                load_a(a, s + AHEAD, end);
-                load_x(a, s + AHEAD, end);
+            if (AHEAD > 1 && s + AHEAD < end) {
+#pragma unroll
+                for (int u = 0; u < AHEAD; ++u) {
+                    load_a(a, u, s + AHEAD + u, end);
+#pragma unroll
+                    for (int q = 0; q < TT; ++q) load_x(a, u, q, s + AHEAD + u, end);
+                }
+                hold_loads();
             }
         }
     }
 };
+
+// The rows of v of a run and part of K, for accesses that other workgroups of the launch
+// see and whose whole 16 bytes count as one.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t v_rows(const LoraArgs& a, const Run& run, int split) {
+    return __builtin_amdgcn_make_buffer_rsrc(a.v + (static_cast<size_t>(split) * a.T + run.r0) * a.r, 0, kHalfRows * a.r * 4, 4 << 15);
+}
 
 // The workgroup's part `split` of K and ranks from j0 on.  The waves' sums are
 // added in wave order; v is read by other workgroups of this launch.
@@ -190,22 +215,19 @@ __device__ __forceinline__ void make_v(const LoraArgs& a, const Run& run, int sp
     Sums<RF, TT, (RF + TT <= 2 ? 2 : 1)> sums;
     sums.begin(a, run, j0, beg, end);
     sums.run_steps(a, beg, end);
-    float* v = a.v + static_cast<size_t>(split) * a.T * a.r;
+    const auto to = v_rows(a, run, split);
 #pragma unroll
     for (int i = 0; i < RF * TT; ++i) part[(wave * RF * TT + i) * kWave + lane] = sums.acc[i];
     __syncthreads();
+    // four ranks of a token, neighbouring threads in a row; r is a multiple of 8
     for (int i = threadIdx.x; i < RF * TT * kWave; i += kWaves * kWave) {
+        const int row = i / (4 * RF), quad = i % (4 * RF), j = j0 + 4 * quad;
+        const int from = (quad / 4 * TT + row / 16) * kWave + 16 * (quad % 4) + row % 16;
         f32x4 s = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) s += part[w * RF * TT * kWave + i];
-        // four ranks of one token; r is a multiple of 8
-        const int l = i % kWave, row = run.r0 + 16 * (i / kWave % TT) + l % 16, j = j0 + 16 * (i / kWave / TT) + 4 * (l / 16);
-        if (row >= run.r1 || j >= a.r) continue;
-        unsigned long long* to = reinterpret_cast<unsigned long long*>(v + static_cast<size_t>(row) * a.r + j);
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-            __hip_atomic_store(to + h, static_cast<unsigned long long>(__float_as_uint(s[2 * h + 1])) << 32 | __float_as_uint(s[2 * h]),
-                               __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        for (int w = 0; w < kWaves; ++w) s += part[w * RF * TT * kWave + from];
+        if (run.r0 + row < run.r1 && j < a.r)
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, s), to, (row * a.r + j) * 4, 0, kAuxDevice);
     }
 }
 
@@ -453,6 +475,7 @@ __device__ __forceinline__ void make_columns(const LoraArgs& a, const Run& run, 
 #pragma unroll
     for (int q = 0; q < TT; ++q) load_base<F32, VEC>(a, t[q], col, base[q]);
     w[0].put(a, 0, share);
+    if (KS > kHeld && 32 * kHeld < a.r) w[0].load(a, run.g, n0, kHeld);
     hold_loads();
     if (threadIdx.x < kWave) {
         const bool there = wait_flags(flags, n, chain_tag());
@@ -460,31 +483,37 @@ __device__ __forceinline__ void make_columns(const LoraArgs& a, const Run& run, 
     }
     __syncthreads();
     const float from = *given_up ? NAN : 0.f;
-    // v, its parts of K added in order; zeros past the run and past r
-    for (int i = threadIdx.x; i < 16 * TT * 8 * KS; i += kWaves * kWave) {
-        const int row = i / (8 * KS), j = i % (8 * KS) * 4;
-        const bool live = run.r0 + row < run.r1 && j < a.r;
-        const float* v = a.v + (live ? static_cast<size_t>(run.r0 + row) * a.r + j : 0);
-        unsigned long long part[kMostSplits][2];
+    // v, its parts of K added in order; zeros past the run and past r.  A thread has kMine
+    // times four ranks, of which it asks for up to eight parts at once.
+    constexpr int kQuads = 16 * TT * 8 * KS, kMine = (kQuads + kWaves * kWave - 1) / (kWaves * kWave);
+    constexpr int kAtOnce = kMine < kMostSplits ? kMostSplits / kMine : 1;
+    auto quad = [&](int i) { return i * kWaves * kWave + static_cast<int>(threadIdx.x); };
+    auto live = [&](int i) { return run.r0 + quad(i) / (8 * KS) < run.r1 && quad(i) % (8 * KS) * 4 < a.r; };
+    f32x4 sum[kMine];
 #pragma unroll
-        for (int s = 0; s < kMostSplits; ++s) {
-            if (s >= a.splits) break;
-            const unsigned long long* p = reinterpret_cast<const unsigned long long*>(v + static_cast<size_t>(s) * a.T * a.r);
+    for (int i = 0; i < kMine; ++i) sum[i] = f32x4{from, from, from, from};
+    for (int s0 = 0; s0 < a.splits; s0 += kAtOnce) {
+        u32x4 part[kAtOnce][kMine];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) part[s][h] = __hip_atomic_load(p + h, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        for (int s = 0; s < kAtOnce; ++s) {
+            if (s0 + s >= a.splits) break;
+            const auto v = v_rows(a, run, s0 + s);
+#pragma unroll
+            for (int i = 0; i < kMine; ++i)
+                part[s][i] = __builtin_amdgcn_raw_buffer_load_b128(
+                    v, live(i) ? (quad(i) / (8 * KS) * a.r + quad(i) % (8 * KS) * 4) * 4 : 0, 0, kAuxDevice);
         }
-        f32x4 sum = {from, from, from, from};
 #pragma unroll
-        for (int s = 0; s < kMostSplits; ++s) {
-            if (s >= a.splits) break;
+        for (int s = 0; s < kAtOnce; ++s) {
+            if (s0 + s >= a.splits) break;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                sum[2 * h] += __uint_as_float(static_cast<uint32_t>(part[s][h]));
-                sum[2 * h + 1] += __uint_as_float(static_cast<uint32_t>(part[s][h] >> 32));
-            }
+            for (int i = 0; i < kMine; ++i) sum[i] += __builtin_bit_cast(f32x4, part[s][i]);
         }
-        parts.set(row, j, live ? sum : f32x4{0.f, 0.f, 0.f, 0.f});
     }
+#pragma unroll
+    for (int i = 0; i < kMine; ++i)
+        if (kQuads % (kWaves * kWave) == 0 || quad(i) < kQuads)
+            parts.set(quad(i) / (8 * KS), quad(i) % (8 * KS) * 4, live(i) ? sum[i] : f32x4{0.f, 0.f, 0.f, 0.f});
     __syncthreads();
 #pragma unroll
     for (int q0 = 0; q0 < TT; q0 += kTogether) {
@@ -493,12 +522,15 @@ __device__ __forceinline__ void make_columns(const LoraArgs& a, const Run& run, 
         for (int q = 0; q < kTogether; ++q)
 #pragma unroll
             for (int f = 0; f < 8; ++f) acc[q][f] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll kHeld
+#pragma unroll
         for (int s = 0; s < KS; ++s) {
             if (32 * s >= a.r) break;
             // the wave's own share, in order: no barrier
-            if (s) w[s % kHeld].put(a, s, share);
-            if (KS > kHeld && 32 * (s + kHeld) < a.r) w[s % kHeld].load(a, run.g, n0, s + kHeld);
+            if (s) {
+                w[s % kHeld].put(a, s, share);
+                if (KS > kHeld && 32 * (s + kHeld) < a.r) w[s % kHeld].load(a, run.g, n0, s + kHeld);
+                if (KS > kHeld) hold_loads();
+            }
             bf16x8 wo[8];
 #pragma unroll
             for (int f = 0; f < 8; ++f) wo[f] = Weights<VEC>::get(a, s, share, f);
@@ -508,6 +540,16 @@ __device__ __forceinline__ void make_columns(const LoraArgs& a, const Run& run, 
 #pragma unroll
         for (int q = 0; q < kTogether; ++q) store_sum<F32, VEC>(a, t[q0 + q], col, scale, acc[q], base[q0 + q]);
     }
+}
+
+// Workgroups go round the XCDs, whose L2s are apart.  With several blocks of ranks
+// those of two neighbouring halves are on one XCD, so that it alone reads their x, and their
+// a mostly once (2048 tokens x 4096 x 4096, us: rank 64 23.5 -> 22.1, rank 128 35.2 ->
+// 31.8; with four neighbours rank 64 23.5): `big` workgroups are those of 8 kNear halves.
+constexpr int kXcds = 8, kNear = 2;
+__host__ __device__ inline bool near_halves(int halves, int ranks) { return ranks > 1 && halves >= kXcds * kNear; }
+__host__ __device__ inline long long lora_makers(long long halves, int each, bool near) {
+    return near ? (halves + kXcds * kNear - 1) / (kXcds * kNear) * (kXcds * kNear) * each : halves * each;
 }
 
 // The grid: `ranks` blocks of 32 ranks x a.splits parts of K of every half item,
@@ -521,9 +563,17 @@ __global__ __launch_bounds__(kWaves* kWave, KS == 1 ? 3 : KS <= 4 ? 2 : 1) void 
     };
     constexpr size_t kPartBytes = kWaves * 4 * kWave * sizeof(f32x4);
     __shared__ __align__(16) uint8_t lds[sizeof(Columns) > kPartBytes ? sizeof(Columns) : kPartBytes];
-    const int each = a.splits * ranks, makers = a.n_items * kHalves * each;
+    const int each = a.splits * ranks, halves = a.n_items * kHalves;
+    const bool near = near_halves(halves, ranks);
+    const int makers = lora_makers(halves, each, near);
     int at = blockIdx.x;
     if (at < makers) {
+        if (near) {
+            const int big = kXcds * kNear * each, in = at % big, k = in / kXcds;
+            const int half = (at / big * kXcds + in % kXcds) * kNear + k / each;
+            if (half >= halves) return;
+            at = half * each + k % each;
+        }
         const Run run = load_half(a, at / each);
         if (run.g < 0 || run.g == a.L) return;
         f32x4* part = reinterpret_cast<f32x4*>(lds);
@@ -737,7 +787,7 @@ hipError_t launch_few(const LoraArgs& a, hipStream_t st) {
 template <bool F32, bool VEC>
 hipError_t launch(const LoraArgs& a, hipStream_t st) {
     const int n_tiles = ceil_div(a.N, kCols), ranks = ceil_div(a.r, 32), halves = a.n_items * kHalves;
-    const int blocks = halves * (a.splits * ranks + n_tiles);
+    const int blocks = lora_makers(halves, a.splits * ranks, near_halves(halves, ranks)) + halves * n_tiles;
     if (a.r <= 32) lora_kernel<F32, VEC, 1><<<blocks, kWaves * kWave, 0, st>>>(a, n_tiles, ranks);
     else if (a.r <= 64) lora_kernel<F32, VEC, 2><<<blocks, kWaves * kWave, 0, st>>>(a, n_tiles, ranks);
     else if (a.r <= 128) lora_kernel<F32, VEC, 4><<<blocks, kWaves * kWave, 0, st>>>(a, n_tiles, ranks);
@@ -748,10 +798,11 @@ hipError_t launch(const LoraArgs& a, hipStream_t st) {
 }  // namespace
 
 // Few tokens: see few_body (us: four tokens of one adapter at rank 16 6.6, else
-// 6.9; one at rank 32 6.2, 6.3; four 9.2, 6.7; one at rank 64 11.0, 7.7).  Else parts of K until the workgroups that make v are about one and a
-// half a CU (us, twice and four times as many, 4096 x 4096: 512 tokens of 64 adapters at
-// rank 64 17.4 -> 19.8 -> 22.4, 2048 tokens of 8 requests at rank 64 25.2 -> 26.2 ->
-// 31.8, at rank 16 16.8 -> 16.2 -> 16.3), with a step or more for each wave.
+// 6.9; one at rank 32 6.2, 6.3; four 9.2, 6.7; one at rank 64 11.0, 7.7).  Else parts
+// of K until the workgroups that make v are about one and a half a CU (us, and with twice
+// as many, 4096 x 4096: 512 tokens of 64 adapters at rank 64 20.4, 20.0; 2048 of 8 requests
+// at rank 32 16.8, 17.0, at 64 22.0, 24.3, at 128 33.6, 35.4), with a step or more for
+// each wave.
 LoraShape lora_shape(int T, int K, int N, int r, int L) {
     LoraShape p{0, 0, 0};
     if (r <= 32 && T * ceil_div(r, 16) <= 4) return p;
@@ -761,7 +812,7 @@ LoraShape lora_shape(int T, int K, int N, int r, int L) {
     while (p.splits < kMostSplits && 2ll * p.splits * runs * ranks <= 380 && steps >= 2 * p.splits * kWaves) p.splits *= 2;
     const long long halves = static_cast<long long>(plan_items(T, L)) * kHalves;
     p.flags = halves * p.splits * ranks;
-    p.blocks = p.flags + halves * ((static_cast<long long>(N) + kCols - 1) / kCols);
+    p.blocks = lora_makers(halves, p.splits * ranks, near_halves(halves, ranks)) + halves * ((static_cast<long long>(N) + kCols - 1) / kCols);
     return p;
 }
 
