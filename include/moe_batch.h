@@ -70,15 +70,21 @@ int moe_lora_plan(int32_t T, int32_t L, const int32_t* ids, int32_t* offsets, in
    all, or >= N) and out_stride (>= N) values apart; out may be base itself (in
    place, same stride), whose rows of no adapter are then not touched.
    Both sums have the accuracy of fp32 sums of exact products whatever
-   `type`.  A value of v that is not finite makes its token's row non-finite.
+   `type`.  A value of v that is not finite (or not below 2^128 - 2^119) makes
+   its token's row non-finite, one of b its column of its adapter's tokens.
    A rank that is no multiple of 8 is padded with zero rows of a and columns
    of b.  Adapters without tokens are not read.  Entries of perm and items
    outside their ranges are skipped, never followed.
-   ws: moe_lora_add_workspace_bytes(T, K, N, r, L) bytes (0: ws may be NULL),
-   uninitialised; one call at a time.  T == 0 enqueues nothing.
+   ws: moe_lora_add_workspace_bytes(T, K, N, r, L) bytes (0, with few tokens:
+   ws may be NULL), uninitialised; one call at a time.  It holds v, which
+   workgroups hand to others of the same launch by flags; a wait for a flag is
+   bounded, and one that gave up would leave NaN in its rows.  T == 0 enqueues
+   nothing.
    Limits: T and L as moe_lora_plan; K a positive multiple of 32 up to 2^22;
-   1 <= N < 2^30; r a multiple of 8 from 8 to 256; fewer than 2^23 workgroups,
-   one per item and 256 columns at most.  Errors: MOE_ERR_SHAPE, MOE_ERR_NULL,
+   1 <= N < 2^30; r a multiple of 8 from 8 to 256; fewer than 2^23 workgroups:
+   two per item for each 512 columns, and two per item, 32 ranks and part of K
+   (1, 2, 4 or 8 of them, one with many tokens), items * 2 rounded up to 16.
+   Errors: MOE_ERR_SHAPE, MOE_ERR_NULL,
    MOE_ERR_FORMAT (type), MOE_ERR_ALIGN, MOE_ERR_WORKSPACE,
    MOE_ERR_UNSUPPORTED (out is base with another stride), MOE_ERR_HIP. */
 size_t moe_lora_add_workspace_bytes(int32_t T, int32_t K, int32_t N, int32_t r, int32_t L);
@@ -105,8 +111,10 @@ int moe_lora_add(int32_t T, int32_t K, int32_t N, int32_t r, int32_t L, const ui
    probability is -inf, the entropy 0.  A row holding a NaN or +inf: its
    floats are NaN, its top_ids -1.  A token outside [0, V) is not followed:
    its log probability is NaN.
-   ws: moe_token_logprobs_workspace_bytes(T, V, top) bytes (0: ws may be
-   NULL), uninitialised; one call at a time.  T == 0 enqueues nothing.
+   ws: moe_token_logprobs_workspace_bytes(T, V, top) bytes (0, with many rows or
+   short ones: ws may be NULL), uninitialised; one call at a time.  It holds the
+   results of parts of a row, which the workgroup that finds them all there
+   joins; none waits for another.  T == 0 enqueues nothing.
    Limits: 0 <= T < 2^30, 1 <= V < 2^30, 0 <= given <= 4096, 0 <= top <=
    min(V, 64).  Errors: MOE_ERR_SHAPE, MOE_ERR_NULL, MOE_ERR_FORMAT (type),
    MOE_ERR_ALIGN, MOE_ERR_WORKSPACE, MOE_ERR_HIP. */

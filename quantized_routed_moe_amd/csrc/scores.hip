@@ -487,6 +487,7 @@ __device__ __forceinline__ void join_row(const ScoreArgs& a, int t, const char* 
             __syncthreads();
             mine = sh.merged[lane];
         } else {                               // many lists that lie within one another
+            __syncthreads();                   // sh.count is read by all
             TopList list;
             for (int p = wave; p < a.parts; p += kScoreWaves) list.merge(lane < a.top ? load_device(from + p * a.top + lane) : 0);
             merge_waves(sh, list, a.top);
@@ -596,6 +597,7 @@ __device__ __forceinline__ void share_twice(const ScoreArgs& a, const Row<F32>& 
             sort_buf(sh, a.top);
             __syncthreads();
         } else {                               // many equal to the bound: one after the other
+            __syncthreads();                   // sh.count is read by all
             Stats again;
             TopList list;
             wave_share<F32, false, true, kScoreWaves>(a, row, c_beg, c_end, wave, edges, sh.keys[wave], again, list);

@@ -48,13 +48,15 @@ def check_plan(plan, ids, L):
 def lora(base, x, a, b, ids, scales=None):
     """(out, bound) of a token's adapter, g its id:
 
-    v: a wave adds at most ceil(ceil(K/64)/8) steps of 64 exact products, then
-    8 waves and at most 8 parts of K are added; v in three bf16 parts holds it
-    to half a step; 3 r products and one more rounding each for the sum of
-    parts' magnitudes, the factor and the addition to base."""
+    v: a wave adds at most ceil(ceil(K/128)/4) steps of 128 exact products, then
+    4 waves and at most 8 parts of K are added (few tokens: a lane adds at most
+    ceil(ceil(K/128)/8) steps of 4 pairs, off by 2^1.5 halves each, then 34
+    partial sums, which is less); v in three bf16 parts holds it to half a step;
+    3 r products and one more rounding each for the sum of parts' magnitudes,
+    the factor and the addition to base."""
     out, bound = base.double().clone(), torch.zeros_like(base, dtype=torch.float64)
     K, r = a.shape[2], a.shape[1]
-    deep = -(-(-(-K // 64)) // 8) * 64 + 16
+    deep = -(-(-(-K // 128)) // 4) * 128 + 16
     for e in torch.unique(ids).tolist():
         if not 0 <= e < a.shape[0]:
             continue

@@ -51,6 +51,8 @@ def lora(T=4, K=64, N=100, r=16, L=8, x=A, xs=64, a=A, b=A, sc=A, perm=A, items=
     (dict(xs=63), qm.MOE_ERR_SHAPE), (dict(xs=68), qm.MOE_ERR_SHAPE), (dict(xs=32), qm.MOE_ERR_SHAPE), (dict(xs=-64), qm.MOE_ERR_SHAPE),
     (dict(xs=1 << 41), qm.MOE_ERR_SHAPE), (dict(bs=99), qm.MOE_ERR_SHAPE), (dict(os=99), qm.MOE_ERR_SHAPE), (dict(os=0), qm.MOE_ERR_SHAPE),
     (dict(bs=-100), qm.MOE_ERR_SHAPE), (dict(os=1 << 41), qm.MOE_ERR_SHAPE),
+    (dict(T=(1 << 26) - 1, N=1 << 12, bs=1 << 12, os=1 << 12), qm.MOE_ERR_SHAPE),
+    (dict(T=(1 << 26) - 1, r=256), qm.MOE_ERR_SHAPE),                                  # of those that make v
     (dict(T=1 << 22, N=1 << 20, bs=1 << 20, os=1 << 20), qm.MOE_ERR_SHAPE),            # more workgroups than a grid has
     *[(dict([(n, None)]), qm.MOE_ERR_NULL) for n in ("x", "a", "b", "perm", "items", "base", "out")],
     *[(dict([(n, A + 8)]), qm.MOE_ERR_ALIGN) for n in ("x", "a", "b", "items", "base", "out")],
