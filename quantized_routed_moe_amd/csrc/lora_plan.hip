@@ -25,27 +25,40 @@ __device__ __forceinline__ int group_of(const PlanArgs& a, int t) {
     return id >= 0 && id < a.L ? id : a.L;
 }
 
-// Ranks of a wave's 64 * ROUNDS consecutive tokens from t0 on among the
-// wave's tokens of their group, and the wave's counts in cnt[group].
+// Groups of a wave's 64 * ROUNDS consecutive tokens from t0 on; -1 past the last.
 template <int ROUNDS>
-__device__ __forceinline__ void rank_wave(const PlanArgs& a, int t0, volatile int* cnt, int bits, int (&group)[ROUNDS],
-                                          int (&rank)[ROUNDS]) {
-    const int lane = threadIdx.x & 63;
-    const uint64_t below = lane ? ~0ull >> (64 - lane) : 0ull;
+__device__ __forceinline__ void load_groups(const PlanArgs& a, int t0, int (&group)[ROUNDS]) {
 #pragma unroll
     for (int j = 0; j < ROUNDS; ++j) {
-        const int t = t0 + 64 * j + lane;
-        group[j] = t < a.T ? group_of(a, t) : -1;
+        const int t = t0 + 64 * j + static_cast<int>(threadIdx.x & 63);
+        const int g = group_of(a, min(t, a.T - 1));
+        group[j] = t < a.T ? g : -1;
     }
+}
+
+// Their ranks among the wave's tokens of their group, and the wave's counts in
+// cnt[group].
+template <int ROUNDS>
+__device__ __forceinline__ void rank_wave(const int (&group)[ROUNDS], volatile int* cnt, int bits, int (&rank)[ROUNDS]) {
+    const int lane = threadIdx.x & 63;
+    const uint64_t below = lane ? ~0ull >> (64 - lane) : 0ull;
+    // lanes that differ, in halves: a bit's ballot, turned round where the lane's is set
+    uint32_t lo[ROUNDS], hi[ROUNDS];
+#pragma unroll
+    for (int j = 0; j < ROUNDS; ++j) lo[j] = hi[j] = 0u;
+    for (int b = 0; b < bits; ++b)
+#pragma unroll
+        for (int j = 0; j < ROUNDS; ++j) {
+            const uint32_t mine = static_cast<uint32_t>(static_cast<int>(static_cast<uint32_t>(group[j]) << (31 - b)) >> 31);
+            const uint64_t ones = __ballot(mine != 0u);
+            lo[j] |= static_cast<uint32_t>(ones) ^ mine;
+            hi[j] |= static_cast<uint32_t>(ones >> 32) ^ mine;
+        }
 #pragma unroll
     for (int j = 0; j < ROUNDS; ++j) {
         const int g = group[j];
-        uint64_t same = __ballot(g >= 0);
-        if (g < 0) same = ~same;
-        for (int b = 0; b < bits; ++b) {
-            const uint64_t ones = __ballot((g >> b) & 1);
-            same &= (g >> b) & 1 ? ones : ~ones;
-        }
+        const uint64_t there = __ballot(g >= 0);
+        const uint64_t same = ~(static_cast<uint64_t>(hi[j]) << 32 | lo[j]) & (g >= 0 ? there : ~there);
         // every lane reads before the group's highest lane writes: one wave,
         // whose LDS accesses are in order
         const int before = g >= 0 ? cnt[g] : 0;
@@ -54,27 +67,34 @@ __device__ __forceinline__ void rank_wave(const PlanArgs& a, int t0, volatile in
     }
 }
 
-// Exclusive scan of v over the workgroup's threads; *total in every thread.
+// Exclusive scans of v over the workgroup's threads; total: in every thread.
 template <int WAVES>
-__device__ __forceinline__ int block_scan(int v, int* part, int* total) {
+__device__ __forceinline__ int2 block_scan(int2 v, int2* part, int2& total) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    int incl = v;
+    int2 incl = v;
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
-        const int u = __shfl_up(incl, o);
-        if (lane >= o) incl += u;
+        const int x = __shfl_up(incl.x, o), y = __shfl_up(incl.y, o);
+        if (lane >= o) {
+            incl.x += x;
+            incl.y += y;
+        }
     }
-    __syncthreads();
     if (lane == 63) part[wave] = incl;
     __syncthreads();
-    int base = 0, sum = 0;
+    int2 base = make_int2(0, 0), sum = make_int2(0, 0);
 #pragma unroll
     for (int w = 0; w < WAVES; ++w) {
-        if (w < wave) base += part[w];
-        sum += part[w];
+        const int2 p = part[w];
+        if (w < wave) {
+            base.x += p.x;
+            base.y += p.y;
+        }
+        sum.x += p.x;
+        sum.y += p.y;
     }
-    *total = sum;
-    return base + incl - v;
+    total = sum;
+    return make_int2(base.x + incl.x - v.x, base.y + incl.y - v.y);
 }
 
 __device__ __forceinline__ void store_item(const PlanArgs& a, int at, int g, int first, int end) {
@@ -86,17 +106,16 @@ __device__ __forceinline__ int item_count(int tokens) { return (tokens + kItemRo
 // Offsets and first items of the groups from their totals in LDS, which they
 // replace; unused items.  All threads; PER consecutive groups a thread.
 template <int WAVES>
-__device__ __forceinline__ void scan_groups(const PlanArgs& a, int* tokens, int* first_item, int* part) {
+__device__ __forceinline__ void scan_groups(const PlanArgs& a, int* tokens, int* first_item, int2* part) {
     const int G = a.L + 1, per = (G + WAVES * 64 - 1) / (WAVES * 64);
     const int g0 = min(static_cast<int>(threadIdx.x) * per, G), g1 = min(g0 + per, G);
-    int n = 0, m = 0;
+    int2 n = make_int2(0, 0), all;             // tokens and items
     for (int g = g0; g < g1; ++g) {
-        n += tokens[g];
-        m += item_count(tokens[g]);
+        n.x += tokens[g];
+        n.y += item_count(tokens[g]);
     }
-    int all, used;
-    int at = block_scan<WAVES>(n, part, &all);
-    int item = block_scan<WAVES>(m, part, &used);
+    const int2 before = block_scan<WAVES>(n, part, all);
+    int at = before.x, item = before.y;
     for (int g = g0; g < g1; ++g) {
         const int c = tokens[g];
         tokens[g] = at;
@@ -106,24 +125,26 @@ __device__ __forceinline__ void scan_groups(const PlanArgs& a, int* tokens, int*
         item += item_count(c);
     }
     if (threadIdx.x == 0) {
-        tokens[G] = all;
-        a.offsets[G] = all;
+        tokens[G] = all.x;
+        a.offsets[G] = all.x;
     }
-    for (int i = used + threadIdx.x; i < a.n_items; i += WAVES * 64) store_item(a, i, -1, 0, 0);
+    for (int i = all.y + threadIdx.x; i < a.n_items; i += WAVES * 64) store_item(a, i, -1, 0, 0);
 }
 
 // Up to WAVES * ROUNDS * 64 tokens.
 template <int WAVES, int ROUNDS>
 __global__ __launch_bounds__(WAVES* kWave) void plan_kernel(PlanArgs a, int bits) {
     __shared__ int cnt[WAVES * kMostGroups];   // [WAVES][G], then each wave's first place in the group
-    __shared__ int start[kMostGroups + 1], first_item[kMostGroups], part[WAVES];
+    __shared__ int start[kMostGroups + 1], first_item[kMostGroups];
+    __shared__ int2 part[WAVES];
     __shared__ int sorted[WAVES * ROUNDS * kWave];             // perm, from where it is written in order
     const int G = a.L + 1, wave = threadIdx.x >> 6;
-    for (int i = threadIdx.x; i < WAVES * G; i += WAVES * kWave) cnt[i] = 0;
-    __syncthreads();
     int group[ROUNDS], rank[ROUNDS];
     const int t0 = wave * ROUNDS * kWave;
-    rank_wave<ROUNDS>(a, t0, cnt + wave * G, bits, group, rank);
+    load_groups(a, t0, group);
+    for (int i = threadIdx.x; i < WAVES * G; i += WAVES * kWave) cnt[i] = 0;
+    __syncthreads();
+    rank_wave(group, cnt + wave * G, bits, rank);
     __syncthreads();
     for (int g = threadIdx.x; g < G; g += WAVES * kWave) {
         int sum = 0;
@@ -167,7 +188,8 @@ __global__ __launch_bounds__(kBlockWaves* kWave) void plan_count_kernel(PlanArgs
 
 // One workgroup: a block's counts become its first places in the groups.
 __global__ __launch_bounds__(kBlockWaves* kWave) void plan_scan_kernel(PlanArgs a, int blocks) {
-    __shared__ int start[kMostGroups + 1], first_item[kMostGroups], part[kBlockWaves];
+    __shared__ int start[kMostGroups + 1], first_item[kMostGroups];
+    __shared__ int2 part[kBlockWaves];
     constexpr int kAhead = 16;                 // counts on their way at a time
     const int G = a.L + 1;
     for (int g = threadIdx.x; g < G; g += blockDim.x) {
@@ -194,11 +216,12 @@ __global__ __launch_bounds__(kBlockWaves* kWave) void plan_scan_kernel(PlanArgs 
 __global__ __launch_bounds__(kBlockWaves* kWave) void plan_place_kernel(PlanArgs a, int bits) {
     __shared__ int lds[kBlockWaves * kMostGroups];     // as plan_kernel's cnt
     const int G = a.L + 1, wave = threadIdx.x >> 6;
-    for (int i = threadIdx.x; i < kBlockWaves * G; i += blockDim.x) lds[i] = 0;
-    __syncthreads();
     int group[kBlockRounds], rank[kBlockRounds];
     const int t0 = blockIdx.x * kPlanBlock + wave * kBlockRounds * kWave;
-    rank_wave<kBlockRounds>(a, t0, lds + wave * G, bits, group, rank);
+    load_groups(a, t0, group);
+    for (int i = threadIdx.x; i < kBlockWaves * G; i += blockDim.x) lds[i] = 0;
+    __syncthreads();
+    rank_wave(group, lds + wave * G, bits, rank);
     __syncthreads();
     for (int g = threadIdx.x; g < G; g += blockDim.x) {
         int sum = a.counts[static_cast<size_t>(blockIdx.x) * G + g];
@@ -227,7 +250,9 @@ hipError_t launch_lora_plan(const PlanArgs& a, hipStream_t st) {
     int bits = 1;
     while (a.L >> bits) ++bits;
     if (a.T <= kPlanBlock) {
+        // us: 64 tokens 3.0 (300 in sixteen waves 4.3); 300 in two rounds 4.3, in eight 6.7; 2048 4.6, 7.2
         if (a.T <= 256) plan_kernel<4, 1><<<1, 4 * kWave, 0, st>>>(a, bits);
+        else if (a.T <= 2048) plan_kernel<kBlockWaves, 2><<<1, kBlockWaves * kWave, 0, st>>>(a, bits);
         else plan_kernel<kBlockWaves, kBlockRounds><<<1, kBlockWaves * kWave, 0, st>>>(a, bits);
         return hipGetLastError();
     }
