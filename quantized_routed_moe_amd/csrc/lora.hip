@@ -359,13 +359,15 @@ struct Weights {
     struct Share {
         uint8_t b[8 * f_bytes];
     };
-    // chunks of a row in step s, and at / chunks for at < 512
-    static __device__ __forceinline__ int chunks_of(const LoraArgs& a, int s) { return min(a.r - 32 * s, 32) / 8; }
+    // Chunks of 16 bytes of a row in step s, and at / chunks for at < 512.  FULL: four.
+    template <bool FULL>
+    static __device__ __forceinline__ int chunks_of(const LoraArgs& a, int s) { return FULL ? 4 : min(a.r - 32 * s, 32) / 8; }
     static __device__ __forceinline__ int row_of(int at, int chunks) {
         return at * (chunks == 4 ? 16384 : chunks == 3 ? 21846 : chunks == 2 ? 32768 : 65536) >> 16;
     }
-    __device__ __forceinline__ void load(const LoraArgs& a, int g, int n0, int s) {
-        const int lane = threadIdx.x & 63, chunks = chunks_of(a, s);
+    template <bool FULL>
+    __device__ __forceinline__ void load_rows(const LoraArgs& a, int g, int n0, int s) {
+        const int lane = threadIdx.x & 63, chunks = chunks_of<FULL>(a, s);
         const uint16_t* from = a.b + static_cast<size_t>(g) * a.N * a.r + 32 * s;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -374,8 +376,9 @@ struct Weights {
             v[i] = *reinterpret_cast<const u32x4*>(from + static_cast<size_t>(min(n0 + row, a.N - 1)) * a.r + 8 * (at - row * chunks));
         }
     }
-    __device__ __forceinline__ void put(const LoraArgs& a, int s, Share& to) const {
-        const int lane = threadIdx.x & 63, chunks = chunks_of(a, s);
+    template <bool FULL>
+    __device__ __forceinline__ void put_rows(const LoraArgs& a, int s, Share& to) const {
+        const int lane = threadIdx.x & 63, chunks = chunks_of<FULL>(a, s);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             if (64 * i >= 128 * chunks) break;
@@ -383,6 +386,24 @@ struct Weights {
             const int f = VEC ? row % 8 : row / 16, c = VEC ? row / 8 : row % 16;
             *reinterpret_cast<u32x4*>(to.b + f * f_bytes + c * row_bytes + 16 * (at - row * chunks)) = v[i];
         }
+    }
+    // Whether step s takes the way of four chunks, which does without branches (2048 tokens
+    // x 4096 x 4096, us: rank 64 22.0 -> 21.4, rank 256 70 -> 60; but rank 16 is a bit
+    // slower with both ways in the code, and at rank 128 in fp32 it cost registers: 40 ->
+    // 54).  A kernel of KS > 1 steps has more than 16 KS ranks.
+    template <int KS>
+    static __device__ __forceinline__ bool full(const LoraArgs& a, int s) {
+        return KS != 1 && KS != 4 && (2 * (s + 1) <= KS || 32 * (s + 1) <= a.r);
+    }
+    template <int KS>
+    __device__ __forceinline__ void load(const LoraArgs& a, int g, int n0, int s) {
+        if (full<KS>(a, s)) load_rows<true>(a, g, n0, s);
+        else load_rows<false>(a, g, n0, s);
+    }
+    template <int KS>
+    __device__ __forceinline__ void put(const LoraArgs& a, int s, Share& to) const {
+        if (full<KS>(a, s)) put_rows<true>(a, s, to);
+        else put_rows<false>(a, s, to);
     }
     static __device__ __forceinline__ bf16x8 get(const LoraArgs& a, int s, const Share& from, int f) {
         const int lane = threadIdx.x & 63, j = lane >> 4;
@@ -468,14 +489,14 @@ __device__ __forceinline__ void make_columns(const LoraArgs& a, const Run& run, 
     Eight<F32, VEC> base[TT][4];
 #pragma unroll
     for (int s = 0; s < kHeld; ++s)
-        if (32 * s < a.r) w[s].load(a, run.g, n0, s);
+        if (32 * s < a.r) w[s].template load<KS>(a, run.g, n0, s);
 #pragma unroll
     for (int q = 0; q < TT; ++q) t[q].load(a, run, run.r0 + 16 * q);
     const float scale = a.scales ? a.scales[run.g] : 1.f;
 #pragma unroll
     for (int q = 0; q < TT; ++q) load_base<F32, VEC>(a, t[q], col, base[q]);
-    w[0].put(a, 0, share);
-    if (KS > kHeld && 32 * kHeld < a.r) w[0].load(a, run.g, n0, kHeld);
+    w[0].template put<KS>(a, 0, share);
+    if (KS > kHeld && 32 * kHeld < a.r) w[0].template load<KS>(a, run.g, n0, kHeld);
     hold_loads();
     if (threadIdx.x < kWave) {
         const bool there = wait_flags(flags, n, chain_tag());
@@ -527,8 +548,8 @@ __device__ __forceinline__ void make_columns(const LoraArgs& a, const Run& run, 
             if (32 * s >= a.r) break;
             // the wave's own share, in order: no barrier
             if (s) {
-                w[s % kHeld].put(a, s, share);
-                if (KS > kHeld && 32 * (s + kHeld) < a.r) w[s % kHeld].load(a, run.g, n0, s + kHeld);
+                w[s % kHeld].template put<KS>(a, s, share);
+                if (KS > kHeld && 32 * (s + kHeld) < a.r) w[s % kHeld].template load<KS>(a, run.g, n0, s + kHeld);
                 if (KS > kHeld) hold_loads();
             }
             bf16x8 wo[8];
