@@ -705,6 +705,13 @@ def _moe_type(dtype, name: str) -> int:
     raise ValueError(f"{name} has dtype {dtype}, expected torch.bfloat16 or torch.float32")
 
 
+def _sizes(where: str, *n: int) -> None:
+    """The C entry points take sizes of 32 bits, and ctypes cuts off what is
+    longer: a size that does not fit is refused here."""
+    if max(n) > 0x7fffffff or min(n) < -0x80000000:
+        raise MoeError(MOE_ERR_SHAPE, where)
+
+
 def _elsewhere(dev, stream, where: str):
     """None when a call on device number `dev` can go to the current stream,
     else the scope (of that device, and of `stream` if given) to make it in:
@@ -1010,6 +1017,7 @@ class LoraPlan:
         dev = perm.get_device()
         if dev < 0:
             raise ValueError("LoraPlan takes device tensors")
+        _sizes("LoraPlan", T, adapters)
         self.T, self.adapters, self.dev = T, adapters, dev
         self.perm, self.offsets, self.items = perm, offsets, items
         self.perm_addr = _addr(perm, i32, (T,), dev, "perm")
@@ -1027,6 +1035,7 @@ def lora_plan(ids, adapters: int, *, stream=None) -> LoraPlan:
             return lora_plan(ids, adapters)
     torch = _torch()
     T = ids.numel()
+    _sizes("moe_lora_plan", T, adapters)
     idp = _addr(ids, (torch.int32,), (T,), dev, "ids")
     L = lib()
     n = L.moe_lora_items(T, adapters)
@@ -1065,6 +1074,7 @@ def lora_add(base, x, a, b, plan: LoraPlan, *, scales=None, out=None, ws=None, s
     bf16 = (torch.bfloat16,)
     T, N = shape = base.shape
     L, r, K = a.shape
+    _sizes("moe_lora_add", T, K, N, r, L)
     if x.dtype != torch.bfloat16 or x.shape != (T, K):
         raise ValueError(f"x must be torch.bfloat16 of shape {(T, K)}")
     if plan.T != T or plan.adapters != L:
@@ -1115,6 +1125,7 @@ def token_logprobs(logits, tokens=None, *, top: int = 0, entropy: bool = False, 
     f32, i32 = torch.float32, torch.int32
     lp, stride = _rows(logits, dev, "logits")
     T, V = logits.shape
+    _sizes("moe_token_logprobs", T, V, top)
     lt = _moe_type(logits.dtype, "logits")
     out = ent = ids = top_lp = None
     tp = outp = entp = idp = tlp = None
@@ -1123,6 +1134,7 @@ def token_logprobs(logits, tokens=None, *, top: int = 0, entropy: bool = False, 
         if tokens.dim() not in (1, 2) or tokens.shape[0] != T:
             raise ValueError(f"tokens must have shape ({T},) or ({T}, n)")
         given = 1 if tokens.dim() == 1 else tokens.shape[1]
+        _sizes("moe_token_logprobs", given)
         tp = _addr(tokens, (i32,), tokens.shape, dev, "tokens")
         out = torch.empty_like(tokens, dtype=f32)
         outp = out.data_ptr()
