@@ -77,9 +77,13 @@ int moe_lora_plan(int32_t T, int32_t L, const int32_t* ids, int32_t* offsets, in
    outside their ranges are skipped, never followed.
    ws: moe_lora_add_workspace_bytes(T, K, N, r, L) bytes (0, with few tokens:
    ws may be NULL), uninitialised; one call at a time.  It holds v, which
-   workgroups hand to others of the same launch by flags; a wait for a flag is
-   bounded, and one that gave up would leave NaN in its rows.  T == 0 enqueues
-   nothing.
+   workgroups hand to others of the same launch by flags; one that waits for a
+   flag longer than about 20 ms (launches on several streams can keep each
+   other's workgroups from their places) makes the v it needs itself, so the
+   result does not depend on it.  T == 0 enqueues nothing.
+   moe_lora_add_polls: the same, with the number of times a workgroup asks for
+   a flag, from 0 (it makes v itself at once) to 2^18, else MOE_ERR_SHAPE.  The
+   result has the same bits; moe_lora_add takes 2^14.
    Limits: T and L as moe_lora_plan; K a positive multiple of 32 up to 2^22;
    1 <= N < 2^30; r a multiple of 8 from 8 to 256; fewer than 2^23 workgroups:
    two per item for each 512 columns, and two per item, 32 ranks and part of K
@@ -92,6 +96,10 @@ int moe_lora_add(int32_t T, int32_t K, int32_t N, int32_t r, int32_t L, const ui
                  const uint16_t* a, const uint16_t* b, const float* scales, const int32_t* perm, const int32_t* items,
                  const void* base, int64_t base_stride, void* out, int64_t out_stride, int32_t type, void* ws,
                  size_t ws_bytes, hipStream_t stream);
+int moe_lora_add_polls(int32_t T, int32_t K, int32_t N, int32_t r, int32_t L, const uint16_t* x, int64_t x_stride,
+                       const uint16_t* a, const uint16_t* b, const float* scales, const int32_t* perm, const int32_t* items,
+                       const void* base, int64_t base_stride, void* out, int64_t out_stride, int32_t type, void* ws,
+                       size_t ws_bytes, int32_t polls, hipStream_t stream);
 
 /* Log probabilities of rows of logits l [V] (log p_v = l_v - log sum e^l):
 

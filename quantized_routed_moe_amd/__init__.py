@@ -67,6 +67,7 @@ EXPORTS = (
     "moe_expert_gate_up_fp8", "moe_layer_fp8_workspace_bytes", "moe_layer_fp8",
     # include/moe_batch.h
     "moe_lora_items", "moe_lora_plan_workspace_bytes", "moe_lora_plan", "moe_lora_add_workspace_bytes", "moe_lora_add",
+    "moe_lora_add_polls",
     "moe_token_logprobs_workspace_bytes", "moe_token_logprobs",
     # include/moe_peak.h
     "moe_peak_stream", "moe_peak_mfma", "moe_peak_hold",
@@ -172,6 +173,7 @@ def lib() -> ctypes.CDLL:
             "moe_lora_plan": (_I, [_I, _I, _P, _P, _P, _P, _P, _SZ, _P]),
             "moe_lora_add_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I]),
             "moe_lora_add": (_I, [_I, _I, _I, _I, _I, _P, _I64, _P, _P, _P, _P, _P, _P, _I64, _P, _I64, _I, _P, _SZ, _P]),
+            "moe_lora_add_polls": (_I, [_I, _I, _I, _I, _I, _P, _I64, _P, _P, _P, _P, _P, _P, _I64, _P, _I64, _I, _P, _SZ, _I, _P]),
             "moe_token_logprobs_workspace_bytes": (_SZ, [_I, _I, _I]),
             "moe_token_logprobs": (_I, [_I, _I, _P, _I, _I64, _P, _I, _P, _P, _I, _P, _P, _P, _SZ, _P]),
             "moe_peak_stream": (_I, [_P, _SZ, ctypes.c_int32, _P, _P]),

@@ -30,6 +30,7 @@ bool lora_ok(int T, int K, int N, int r, int L) {
 }
 
 constexpr long long kMostBlocks = 1ll << 23;   // of 256 threads or 512: a grid holds fewer than 2^32
+constexpr int kMostPolls = 1 << 18;
 
 bool scores_ok(int T, int V, int top) {
     return T >= 0 && T < kDimLimit && V >= 1 && V < kDimLimit && top >= 0 && top <= kMostTop && top <= V;
@@ -83,7 +84,15 @@ int moe_lora_add(int32_t T, int32_t K, int32_t N, int32_t r, int32_t L, const ui
                  const uint16_t* a, const uint16_t* b, const float* scales, const int32_t* perm, const int32_t* items,
                  const void* base, int64_t base_stride, void* out, int64_t out_stride, int32_t type, void* ws,
                  size_t ws_bytes, hipStream_t stream) {
-    if (!lora_ok(T, K, N, r, L)) return MOE_ERR_SHAPE;
+    return moe_lora_add_polls(T, K, N, r, L, x, x_stride, a, b, scales, perm, items, base, base_stride, out, out_stride, type,
+                              ws, ws_bytes, kLoraPolls, stream);
+}
+
+int moe_lora_add_polls(int32_t T, int32_t K, int32_t N, int32_t r, int32_t L, const uint16_t* x, int64_t x_stride,
+                       const uint16_t* a, const uint16_t* b, const float* scales, const int32_t* perm, const int32_t* items,
+                       const void* base, int64_t base_stride, void* out, int64_t out_stride, int32_t type, void* ws,
+                       size_t ws_bytes, int32_t polls, hipStream_t stream) {
+    if (!lora_ok(T, K, N, r, L) || polls < 0 || polls > kMostPolls) return MOE_ERR_SHAPE;
     if (T == 0) return MOE_OK;
     if (!x || !a || !b || !perm || !items || !base || !out) return MOE_ERR_NULL;
     if (!known_type(type)) return MOE_ERR_FORMAT;
@@ -123,6 +132,7 @@ int moe_lora_add(int32_t T, int32_t K, int32_t N, int32_t r, int32_t L, const ui
     p.splits = shape.splits;
     p.v = static_cast<float*>(ws);
     p.flags = reinterpret_cast<unsigned long long*>(static_cast<char*>(ws) + lora_v_bytes(shape, T, r));
+    p.polls = polls;
     return hip_rc(launch_lora_add(p, stream));
 }
 

@@ -62,7 +62,13 @@ struct LoraArgs {
     int splits;
     float* v;                                  // [splits][T][r], by entry of perm
     unsigned long long* flags;
+    int polls;                                 // of a wait for v, 0: none
+    int tid;                                   // of the kernel: threadIdx.x
 };
+
+// About 20 ms, far beyond what v of one run takes (K of 2^22: 1 ms), and a sixteenth of
+// the layer's bound: what waits here makes room before a layer beside it gives up.
+constexpr int kLoraPolls = 1 << 14;
 
 hipError_t launch_lora_add(const LoraArgs& a, hipStream_t st);
 

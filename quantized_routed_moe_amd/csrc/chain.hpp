@@ -17,8 +17,11 @@
 // Progress: consumers are placed after all their producers in the grid, and
 // producers never wait.  Workgroups are handed to the XCDs round-robin and
 // dispatched in id order within each XCD, so a waiting consumer never holds
-// CU resources that a not yet dispatched producer needs.  Every wait is
-// bounded all the same (kMaxPolls; MOE_DEV_CHAIN_TIMEOUT when exceeded).
+// CU resources that a not yet dispatched producer needs.  That holds within one
+// launch: two on different streams can each fill an XCD with waiting consumers
+// on which the other's producers have no place yet.  So every wait is bounded
+// (kMaxPolls; MOE_DEV_CHAIN_TIMEOUT when exceeded; the adapters' consumers wait
+// a sixteenth of it and then do without, which frees the others).
 #pragma once
 
 #include "common.hpp"

@@ -7,9 +7,9 @@
 // ranks and a part of K, which their waves split, their sums meeting in LDS in wave
 // order.  Then those of the columns: up to 32 tokens of a run x 512 columns, whose
 // weights and base are on their way while they wait for v by its flags; they add
-// its parts in order, so nothing depends on timing.  (In two launches 2048 tokens x
-// 4096 x 4096 at rank 32 took 21.2 us, in one 16.9; 64 tokens of 64 adapters at rank
-// 16 10.2 and 8.6.)
+// its parts in order, so nothing depends on timing.  One that has waited long makes
+// its tokens' v itself.  (In two launches 2048 tokens x 4096 x 4096 at rank 32 took
+// 21.2 us, in one 16.9; 64 tokens of 64 adapters at rank 16 10.2 and 8.6.)
 //
 // Both are 16x16x32 bf16 products, exact in fp32 but for the sums.  v is fp32: for
 // the columns it is split into three bf16 parts that hold its 24 bits, and three
@@ -103,7 +103,7 @@ struct Sums {
 
     // Rows, and the first steps' loads.
     __device__ __forceinline__ void begin(const LoraArgs& a, const Run& run, int j0, int beg, int end) {
-        const int row = threadIdx.x & 12;
+        const int row = a.tid & 12;
         int t[TT][4];
 #pragma unroll
         for (int q = 0; q < TT; ++q)
@@ -208,7 +208,7 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t v_rows(const LoraArgs& a, cons
 // added in wave order; v is read by other workgroups of this launch.
 template <int RF, int TT>
 __device__ __forceinline__ void make_v(const LoraArgs& a, const Run& run, int split, int j0, f32x4* part) {
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int lane = a.tid & 63, wave = __builtin_amdgcn_readfirstlane(a.tid >> 6);
     const long long steps = ceil_div(a.K, kStep);
     const int slice = split * kWaves + wave, slices = a.splits * kWaves;
     const int beg = steps * slice / slices, end = steps * (slice + 1) / slices;
@@ -220,7 +220,7 @@ __device__ __forceinline__ void make_v(const LoraArgs& a, const Run& run, int sp
     for (int i = 0; i < RF * TT; ++i) part[(wave * RF * TT + i) * kWave + lane] = sums.acc[i];
     __syncthreads();
     // four ranks of a token, neighbouring threads in a row; r is a multiple of 8
-    for (int i = threadIdx.x; i < RF * TT * kWave; i += kWaves * kWave) {
+    for (int i = a.tid; i < RF * TT * kWave; i += kWaves * kWave) {
         const int row = i / (4 * RF), quad = i % (4 * RF), j = j0 + 4 * quad;
         const int from = (quad / 4 * TT + row / 16) * kWave + 16 * (quad % 4) + row % 16;
         f32x4 s = {0.f, 0.f, 0.f, 0.f};
@@ -367,7 +367,7 @@ struct Weights {
     }
     template <bool FULL>
     __device__ __forceinline__ void load_rows(const LoraArgs& a, int g, int n0, int s) {
-        const int lane = threadIdx.x & 63, chunks = chunks_of<FULL>(a, s);
+        const int lane = a.tid & 63, chunks = chunks_of<FULL>(a, s);
         const uint16_t* from = a.b + static_cast<size_t>(g) * a.N * a.r + 32 * s;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -378,7 +378,7 @@ struct Weights {
     }
     template <bool FULL>
     __device__ __forceinline__ void put_rows(const LoraArgs& a, int s, Share& to) const {
-        const int lane = threadIdx.x & 63, chunks = chunks_of<FULL>(a, s);
+        const int lane = a.tid & 63, chunks = chunks_of<FULL>(a, s);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             if (64 * i >= 128 * chunks) break;
@@ -406,7 +406,7 @@ struct Weights {
         else put_rows<false>(a, s, to);
     }
     static __device__ __forceinline__ bf16x8 get(const LoraArgs& a, int s, const Share& from, int f) {
-        const int lane = threadIdx.x & 63, j = lane >> 4;
+        const int lane = a.tid & 63, j = lane >> 4;
         // past r: any ranks, their v are zeros
         const int chunk = 32 * s + 8 * j < a.r ? j : 0;
         return *reinterpret_cast<const bf16x8*>(from.b + f * f_bytes + (lane & 15) * row_bytes + 16 * chunk);
@@ -417,7 +417,7 @@ struct Weights {
 struct Tokens {
     int t[4];
     __device__ __forceinline__ void load(const LoraArgs& a, const Run& run, int first) {
-        const int at = first + 4 * (threadIdx.x >> 4 & 3);
+        const int at = first + 4 * (a.tid >> 4 & 3);
 #pragma unroll
         for (int i = 0; i < 4; ++i) t[i] = a.perm[min(at + i, a.T - 1)];
 #pragma unroll
@@ -475,12 +475,22 @@ __device__ __forceinline__ void copy_rows(const LoraArgs& a, const Run& run, int
     }
 }
 
+// The LDS of a workgroup of columns.
+template <bool VEC, int KS>
+struct Columns {
+    Parts<kHalfRows, KS> parts;
+    typename Weights<VEC>::Share shares[kWaves];
+    int given_up;
+};
+
 // A wave's 128 columns from n0 on of the run's tokens.  TT: tiles of 16 tokens,
-// KS: steps of 32 ranks.  flags: those of the n workgroups that make the tokens' v.
-template <bool F32, bool VEC, int TT, int KS>
-__device__ __forceinline__ void make_columns(const LoraArgs& a, const Run& run, int n0, Parts<kHalfRows, KS>& parts,
-                                             typename Weights<VEC>::Share& share, const unsigned long long* flags, int n,
-                                             int* given_up) {
+// KS: steps of 32 ranks.  flags: those of the n workgroups that make the tokens' v;
+// with WAIT false v is there.  Not 0 if it gave up waiting, with nothing stored.
+template <bool F32, bool VEC, int TT, int KS, bool WAIT>
+__device__ __forceinline__ int make_columns(const LoraArgs& a, const Run& run, int n0, Columns<VEC, KS>& x,
+                                             const unsigned long long* flags, int n) {
+    auto& parts = x.parts;
+    auto& share = x.shares[__builtin_amdgcn_readfirstlane(threadIdx.x >> 6)];
     constexpr int kHeld = KS == 1 ? 1 : 2;     // steps' weights on their way
     constexpr int kTogether = KS == 1 ? 1 : TT;                // tiles whose sums are held over the steps
     const int col = lane_column<VEC>(n0);
@@ -498,21 +508,24 @@ __device__ __forceinline__ void make_columns(const LoraArgs& a, const Run& run, 
     w[0].template put<KS>(a, 0, share);
     if (KS > kHeld && 32 * kHeld < a.r) w[0].template load<KS>(a, run.g, n0, kHeld);
     hold_loads();
-    if (threadIdx.x < kWave) {
-        const bool there = wait_flags(flags, n, chain_tag());
-        if (threadIdx.x == 0) *given_up = !there;
+    if constexpr (WAIT) {
+        if (threadIdx.x < kWave) {
+            const bool there = wait_flags(flags, n, chain_tag(), a.polls);
+            if (threadIdx.x == 0) x.given_up = !there;
+        }
+        __syncthreads();
+        const int up = __builtin_amdgcn_readfirstlane(x.given_up);
+        if (__builtin_expect(up != 0, 0)) return up;
     }
-    __syncthreads();
-    const float from = *given_up ? NAN : 0.f;
     // v, its parts of K added in order; zeros past the run and past r.  A thread has kMine
     // times four ranks, of which it asks for up to eight parts at once.
     constexpr int kQuads = 16 * TT * 8 * KS, kMine = (kQuads + kWaves * kWave - 1) / (kWaves * kWave);
     constexpr int kAtOnce = kMine < kMostSplits ? kMostSplits / kMine : 1;
-    auto quad = [&](int i) { return i * kWaves * kWave + static_cast<int>(threadIdx.x); };
+    auto quad = [&](int i) { return i * kWaves * kWave + a.tid; };
     auto live = [&](int i) { return run.r0 + quad(i) / (8 * KS) < run.r1 && quad(i) % (8 * KS) * 4 < a.r; };
     f32x4 sum[kMine];
 #pragma unroll
-    for (int i = 0; i < kMine; ++i) sum[i] = f32x4{from, from, from, from};
+    for (int i = 0; i < kMine; ++i) sum[i] = f32x4{0.f, 0.f, 0.f, 0.f};
     for (int s0 = 0; s0 < a.splits; s0 += kAtOnce) {
         u32x4 part[kAtOnce][kMine];
 #pragma unroll
@@ -561,6 +574,32 @@ __device__ __forceinline__ void make_columns(const LoraArgs& a, const Run& run, 
 #pragma unroll
         for (int q = 0; q < kTogether; ++q) store_sum<F32, VEC>(a, t[q0 + q], col, scale, acc[q], base[q0 + q]);
     }
+    asm volatile("");                          // the stores' branches end here, not in the return
+    return 0;
+}
+
+// Tile `at` of columns after make_columns gave up: v by this workgroup, 16 ranks of
+// 16 tokens at a time, then the columns.  The same bits, whatever the tile, v's at the
+// place where their maker stores them too.
+template <bool F32, bool VEC, int KS>
+__device__ __forceinline__ void columns_alone(LoraArgs& a, int at, int n_tiles, Columns<VEC, KS>& x) {
+    // nothing that follows from these is held from before: there would be too few registers
+    asm volatile("" : "+v"(a.tid), "+s"(at), "+s"(n_tiles));
+    Run run = load_half(a, at / n_tiles);
+    const int n0 = at % n_tiles * kCols + 128 * __builtin_amdgcn_readfirstlane(a.tid >> 6), end = run.r1;
+    for (; run.r0 < end; run.r0 += 16) {
+        run.r1 = min(end, run.r0 + 16);
+        __syncthreads();                       // LDS is free
+        for (int i = 0, blocks = ceil_div(a.r, 16); i < a.splits * blocks; ++i) {
+            asm volatile("" : "+v"(a.tid));
+            make_v<1, 1>(a, run, i / blocks, i % blocks * 16, reinterpret_cast<f32x4*>(&x));
+            __syncthreads();
+        }
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");       // v is there when all threads are past the barrier
+        __syncthreads();
+        asm volatile("" : "+v"(a.tid));
+        make_columns<F32, VEC, 1, KS, false>(a, run, n0, x, nullptr, 0);
+    }
 }
 
 // Workgroups go round the XCDs, whose L2s are apart.  With several blocks of ranks
@@ -575,15 +614,18 @@ __host__ __device__ inline long long lora_makers(long long halves, int each, boo
 
 // The grid: `ranks` blocks of 32 ranks x a.splits parts of K of every half item,
 // then n_tiles tiles of columns of every half item.
+//
+// A workgroup of columns follows those that make its v in the grid, so alone on the
+// GPU it waits for what runs already.  Beside another such launch it may wait for
+// what does not: of each, columns can hold all of an XCD on which the other's makers
+// have no place yet.  So a wait ends after a.polls polls, the workgroup makes v itself,
+// and no launch depends on another's progress.
 template <bool F32, bool VEC, int KS>
-__global__ __launch_bounds__(kWaves* kWave, KS == 1 ? 3 : KS <= 4 ? 2 : 1) void lora_kernel(LoraArgs a, int n_tiles, int ranks) {
-    struct Columns {
-        Parts<kHalfRows, KS> parts;
-        typename Weights<VEC>::Share shares[kWaves];
-        int given_up;
-    };
+__global__ __launch_bounds__(kWaves* kWave, KS == 1 ? 3 : KS <= 4 ? 2 : 1) void lora_kernel(LoraArgs args, int n_tiles, int ranks) {
+    LoraArgs a = args;
+    a.tid = threadIdx.x;
     constexpr size_t kPartBytes = kWaves * 4 * kWave * sizeof(f32x4);
-    __shared__ __align__(16) uint8_t lds[sizeof(Columns) > kPartBytes ? sizeof(Columns) : kPartBytes];
+    __shared__ __align__(16) uint8_t lds[sizeof(Columns<VEC, KS>) > kPartBytes ? sizeof(Columns<VEC, KS>) : kPartBytes];
     const int each = a.splits * ranks, halves = a.n_items * kHalves;
     const bool near = near_halves(halves, ranks);
     const int makers = lora_makers(halves, each, near);
@@ -619,10 +661,17 @@ __global__ __launch_bounds__(kWaves* kWave, KS == 1 ? 3 : KS <= 4 ? 2 : 1) void 
         if (!a.in_place && n0 < a.N) copy_rows<F32, VEC>(a, run, n0);
         return;
     }
-    Columns& x = *reinterpret_cast<Columns*>(lds);
+    Columns<VEC, KS>& x = *reinterpret_cast<Columns<VEC, KS>*>(lds);
     const unsigned long long* flags = a.flags + static_cast<size_t>(half) * each;
-    if (run.r1 - run.r0 > 16) make_columns<F32, VEC, 2, KS>(a, run, n0, x.parts, x.shares[wave], flags, each, &x.given_up);
-    else make_columns<F32, VEC, 1, KS>(a, run, n0, x.parts, x.shares[wave], flags, each, &x.given_up);
+    int given_up = run.r1 - run.r0 > 16 ? make_columns<F32, VEC, 2, KS, true>(a, run, n0, x, flags, each)
+                                        : make_columns<F32, VEC, 1, KS, true>(a, run, n0, x, flags, each);
+    // The ways meet here in one value that the compiler knows nothing of, and the rare one
+    // lies behind the others' code.  With a return of their own instead, the registers of
+    // both were held over each other and spilled (5 tokens at rank 16 6.6 -> 7.5 us); so
+    // 64 tokens of 64 at rank 16 take 8.0 us with and without this way, 5 tokens 6.75 and 6.6.
+    given_up = __builtin_amdgcn_readfirstlane(given_up);
+    asm volatile("" : "+s"(given_up));
+    if (__builtin_expect(given_up != 0, 0)) columns_alone<F32, VEC, KS>(a, at, n_tiles, x);
 }
 
 // Up to four tokens, every workgroup with the whole of their v (4096 x 4096 at
@@ -778,7 +827,9 @@ __device__ __forceinline__ void few_body(const LoraArgs& a, const Run& run, int 
 }
 
 template <bool F32, int RF>
-__global__ __launch_bounds__(kFewWaves* kWave) void lora_few_kernel(LoraArgs a, int n_tiles) {
+__global__ __launch_bounds__(kFewWaves* kWave) void lora_few_kernel(LoraArgs args, int n_tiles) {
+    LoraArgs a = args;
+    a.tid = threadIdx.x;
     __shared__ __align__(16) float part[4 * kFewWaves * 4 * 16 * RF];
     __shared__ __align__(16) float sums[4 * 16 * RF];
     Run run = load_run(a, blockIdx.x / n_tiles);
