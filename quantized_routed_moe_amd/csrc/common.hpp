@@ -229,6 +229,16 @@ __device__ __forceinline__ float wave_sum_f32(float v) {
     return lane_value(v, 63);
 }
 
+// Between LDS accesses of different lanes of a wave to the same place.  The hardware
+// keeps a wave's LDS accesses in order; the compiler only has to keep each lane's
+// own, and may move one lane's load over another's store without this.  No
+// instruction.
+__device__ __forceinline__ void wave_lds_fence() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
+}
+
 __device__ __forceinline__ void raise_status(uint32_t* status, uint32_t bit) {
     atomicOr(status, bit);
 }

@@ -559,9 +559,11 @@ __device__ __forceinline__ int make_columns(const LoraArgs& a, const Run& run, i
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
             if (32 * s >= a.r) break;
-            // the wave's own share, in order: no barrier
+            // the wave's own share: no barrier
             if (s) {
+                wave_lds_fence();
                 w[s % kHeld].template put<KS>(a, s, share);
+                wave_lds_fence();
                 if (KS > kHeld && 32 * (s + kHeld) < a.r) w[s % kHeld].template load<KS>(a, run.g, n0, s + kHeld);
                 if (KS > kHeld) hold_loads();
             }

@@ -147,10 +147,14 @@ struct TopList {
     // The n <= 64 keys of buf (room for 64), sorted by counting for each those above it.
     __device__ __forceinline__ void sort(Key* buf, int n, int top) {
         const int lane = threadIdx.x & 63;
+        wave_lds_fence();
         const Key k = lane < n ? buf[lane] : 0;
         if (lane >= n) buf[lane] = 0;
+        wave_lds_fence();
         const int at = keys_above(buf, n, k);
-        if (lane < n) buf[at] = k;             // one wave: its reads are before its writes
+        wave_lds_fence();
+        if (lane < n) buf[at] = k;
+        wave_lds_fence();
         mine = lane < n ? buf[lane] : 0;
         refresh(top);
     }
@@ -474,6 +478,7 @@ __device__ __forceinline__ void join_row(const ScoreArgs& a, int t, const char* 
         sh.buf[threadIdx.x] = 0;
         if (wave == 0) sh.merged[lane] = 0;
         if (threadIdx.x == 0) sh.count = 0;
+        wave_lds_fence();
         const int above = keys_above(sh.keys[wave], a.parts, k);               // places differ: only zeros are equal
         const uint64_t hit = __ballot(above == q - 1 && k);
         const Key least = hit ? key_of_lane(k, __ffsll(static_cast<unsigned long long>(hit)) - 1) : 1;
