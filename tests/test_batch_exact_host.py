@@ -1,6 +1,8 @@
 """The inputs of tests/batch_exact.py on the CPU: the definitions give the results
 that they claim, and a mistake planted in them does not pass."""
 
+import math
+
 import pytest
 import torch
 
@@ -57,3 +59,33 @@ def test_mean_square_bound_excludes_fewer_parts():
     for parts, inside in ((3, True), (2, False), (1, False)):
         e = (X.in_parts(v, parts) - v).double().pow(2).mean() / v.double().pow(2).mean()
         assert (float(e) <= X.sum_bound(4096, 4)) == inside
+
+
+def answers(here, logits, tokens, top, seen=None):
+    """What token_logprobs would give if it summed the places `seen`."""
+    seen = here if seen is None else seen
+    ln = torch.log(seen.sum(1).double())[:, None]
+    lp = torch.where(here, 0.0, torch.where(torch.isinf(logits), -math.inf, -X.LOW)).double() - ln
+    order = torch.sort(~here, dim=1, stable=True).indices[:, :top]
+    return lp.gather(1, tokens.long()).float(), ln[:, 0].float(), order.to(torch.int32), lp.gather(1, order).float()
+
+
+@pytest.mark.parametrize("V", [100, 4096, 50001, 128256])
+@pytest.mark.parametrize("kind", ["all", "half", "few", "ends", "chunks"])
+def test_a_value_too_many_or_too_few_does_not_pass(kind, V):
+    g = cpu(V)
+    T, per = 6, 8
+    here, logits = X.counted(g, T, V, F32, kind, per)
+    tokens = torch.cat([here.float().argmax(1, keepdim=True), torch.randint(0, V, (T, 1), generator=g)], 1)
+    X.check_counted(here, logits, tokens, 7, answers(here, logits, tokens, 7))
+    for less in (1, 8):
+        seen = here.clone()
+        row = int(here.sum(1).argmax())
+        seen[row, torch.nonzero(here[row])[-less:, 0]] = False
+        if not seen[row].any():
+            continue
+        for what, got in (("logprobs", 0), ("entropy", 1)):
+            bad = list(answers(here, logits, tokens, 7))
+            bad[got] = answers(here, logits, tokens, 7, seen)[got]
+            with pytest.raises(AssertionError, match=what):
+                X.check_counted(here, logits, tokens, 7, bad)

@@ -1,6 +1,7 @@
 """The operators of a batch of many requests on the GPU at inputs whose results are
 known to the bit (tests/batch_exact.py): all 24 bits of v on every way that hands it
-over; and the mean square of the errors of ordinary inputs."""
+over, and every value of a row on every way that takes it; and the mean square of
+the errors of ordinary inputs."""
 
 import pytest
 import torch
@@ -78,3 +79,45 @@ def test_dot_products_of_few_tokens(T, values, halves):
         over = (got.double() - p.sum(2)).abs() / (X.U32 * p.abs().sum(2))
         worst = max(worst, float(over.max()))
     assert worst <= halves, worst
+
+
+# -------------------------------------------------------------------- scores
+
+# a row a wave; a row a workgroup; seen twice, held and read again; parts of a row, held and read again
+WAYS = [(2051, 4096, BF16), (2050, 1023, F32), (2048, 15, BF16), (600, 333, BF16), (700, 5003, BF16), (1300, 20011, BF16),
+        (700, 16001, BF16), (640, 8003, F32), (9, 50001, BF16), (17, 128256, BF16), (9, 128257, F32), (77, 50001, BF16), (9, 1050001, BF16),
+        (9, 600011, F32)]
+
+
+@pytest.mark.parametrize("kind", ["all", "half", "few", "ends", "chunks"])
+@pytest.mark.parametrize("T,V,dtype", WAYS)
+def test_every_value_of_a_row_counts_once(T, V, dtype, kind):
+    """Rows that begin at every place of 16 bytes, with what lies between them larger than
+    all of theirs."""
+    g = gen(T + V)
+    per = 8 if dtype == BF16 else 4
+    here, l = X.counted(g, T, V, dtype, kind, per)
+    step = V // per * per + per + 1
+    buf = torch.full((T, step), 1e6, device="cuda").to(dtype)
+    buf[:, :V] = l
+    tok = torch.cat([here.float().argmax(1, keepdim=True), torch.randint(0, V, (T, 2), generator=g, device="cuda")], 1).to(I32)
+    for top in (0, 3, 30):
+        top = min(top, V)
+        got = qm.token_logprobs(buf[:, :V], tok, top=top, entropy=top != 3)
+        X.check_counted(here, l, tok, top, got, f"top {top}")
+
+
+@pytest.mark.parametrize("T,V,dtype", [(64, 128256, BF16), (64, 128256, F32), (300, 50001, F32), (1300, 20011, BF16), (2048, 2048, F32)])
+def test_mean_square_of_the_errors_of_scores(T, V, dtype):
+    g = gen(T)
+    l = (2.5 * torch.randn((T, V), generator=g, device="cuda")).to(dtype)
+    tok = torch.randint(0, V, (T, 8), generator=g, device="cuda", dtype=I32)
+    lp, ent, _, _ = qm.token_logprobs(l, tok, entropy=True)
+    e_lp, e_h = [], []
+    b_lp = b_h = 0.0
+    for t in range(0, T, 256):
+        want, H, dlp, dH = X.scores_mean_square(l[t:t + 256])
+        e_lp.append((lp[t:t + 256].double() - want.gather(1, tok[t:t + 256].long())).pow(2).flatten())
+        e_h.append((ent[t:t + 256].double() - H).pow(2))
+        b_lp, b_h = max(b_lp, float(dlp)), max(b_h, float(dH))
+    assert float(torch.cat(e_lp).mean()) <= b_lp and float(torch.cat(e_h).mean()) <= b_h
