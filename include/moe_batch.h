@@ -70,7 +70,8 @@ int moe_lora_plan(int32_t T, int32_t L, const int32_t* ids, int32_t* offsets, in
    all, or >= N) and out_stride (>= N) values apart; out may be base itself (in
    place, same stride), whose rows of no adapter are then not touched.
    Both sums have the accuracy of fp32 sums of exact products whatever
-   `type`.  A value of v that is not finite (or not below 2^128 - 2^119) makes
+   `type`, but for what lies below 2^-126: a product that small, and in a v
+   below 2^-102 the bits that are, may count as 0.  A value of v that is not finite (or not below 2^128 - 2^119) makes
    its token's row non-finite, one of b its column of its adapter's tokens.
    A rank that is no multiple of 8 is padded with zero rows of a and columns
    of b.  Adapters without tokens are not read.  Entries of perm and items

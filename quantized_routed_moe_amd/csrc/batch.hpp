@@ -94,7 +94,7 @@ struct ScoreArgs {
     unsigned long long* flags;                 // [T][parts]
 };
 
-int score_parts(int T, int V, bool f32);       // at most 64
+int score_parts(int T, int V, bool f32);       // at most 32
 ScoreTake score_take(int T, int V, int top, bool f32, int parts);
 inline size_t score_stat_bytes(int T, int parts) { return (static_cast<size_t>(T) * parts * 16 + 255) / 256 * 256; }
 

@@ -81,6 +81,25 @@ def test_dot_products_of_few_tokens(T, values, halves):
     assert worst <= halves, worst
 
 
+@pytest.mark.parametrize("T", [1, 3, 5, 40])
+@pytest.mark.parametrize("scale", [-58, -62, -70])
+def test_values_below_the_normal_range(T, scale):
+    """v of about 2^-116, 2^-124 and 2^-140 and columns that make much of them: lost are at
+    most 2^-126 for each product and each part of a v."""
+    K, N, r, L = 96, 40, 24, 2
+    g = gen(T - scale)
+    x, a, b, base, s = B.lora_case(g, T, K, N, r, L, F32)
+    x, a, b = x * 2.0 ** scale, a * 2.0 ** scale, b * 2.0 ** 100
+    ids = torch.randint(0, L, (T,), generator=g, device="cuda", dtype=I32)
+    base.zero_()
+    got = qm.lora_add(base, x, a, b, qm.lora_plan(ids, L), scales=s)
+    want, bound = B.lora(base, x, a, b, ids, s)
+    lost = (K + 3) * b[ids.long()].double().abs().sum(2) * s[ids.long()].double()[:, None] * 2.0 ** -126
+    B.check_rounded(got, want, bound + lost, F32)
+    if scale == -58:
+        assert float((want.abs() / lost).median()) > 1          # the results are not lost in it
+
+
 # -------------------------------------------------------------------- scores
 
 # a row a wave; a row a workgroup; seen twice, held and read again; parts of a row, held and read again
