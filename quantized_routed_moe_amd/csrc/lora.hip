@@ -9,7 +9,7 @@
 // weights and base are on their way while they wait for v by its flags; they add
 // its parts in order, so nothing depends on timing.  One that has waited long makes
 // its tokens' v itself.  (In two launches 2048 tokens x 4096 x 4096 at rank 32 took
-// 21.2 us, in one 16.9; 64 tokens of 64 adapters at rank 16 10.2 and 8.6.)
+// 21.2 us, in one 16.8; 64 tokens of 64 adapters at rank 16 10.2 and 8.2.)
 //
 // Both are 16x16x32 bf16 products, exact in fp32 but for the sums.  v is fp32: for
 // the columns it is split into three bf16 parts that hold its 24 bits, and three
@@ -388,9 +388,10 @@ struct Weights {
         }
     }
     // Whether step s takes the way of four chunks, which does without branches (2048 tokens
-    // x 4096 x 4096, us: rank 64 22.0 -> 21.4, rank 256 70 -> 60; but rank 16 is a bit
-    // slower with both ways in the code, and at rank 128 in fp32 it cost registers: 40 ->
-    // 54).  A kernel of KS > 1 steps has more than 16 KS ranks.
+    // x 4096 x 4096, us: rank 64 21.7 -> 21.2, rank 256 69 -> 58).  Not where both ways in
+    // the code cost more: 64 tokens of 64 adapters at rank 16 8.2 -> 8.7, and, for want of
+    // registers, 2048 tokens at rank 128 in fp32 42 -> 47 (in bf16 30.9 -> 30.3).  A kernel
+    // of KS > 1 steps has more than 16 KS ranks.
     template <int KS>
     static __device__ __forceinline__ bool full(const LoraArgs& a, int s) {
         return KS != 1 && KS != 4 && (2 * (s + 1) <= KS || 32 * (s + 1) <= a.r);
@@ -606,8 +607,13 @@ __device__ __forceinline__ void columns_alone(LoraArgs& a, int at, int n_tiles, 
 
 // Workgroups go round the XCDs, whose L2s are apart.  With several blocks of ranks
 // those of two neighbouring halves are on one XCD, so that it alone reads their x, and their
-// a mostly once (2048 tokens x 4096 x 4096, us: rank 64 23.5 -> 22.1, rank 128 35.2 ->
-// 31.8; with four neighbours rank 64 23.5): `big` workgroups are those of 8 kNear halves.
+// a mostly once (2048 tokens of 8 requests x 4096 x 4096, us: rank 64 22.3 -> 21.1, rank
+// 128 34.4 -> 31.0, rank 256 58.9 -> 58.1; 512 of 64 adapters, rank 64, 2048 columns, 16.8 ->
+// 16.1; with four neighbours rank 64 as slow as without): `big` workgroups are those of 8
+// kNear halves.  The count is that of all halves the schedule has room for; where few of
+// them have tokens, their makers share few XCDs, and from rank 128 on that costs more than
+// the order gains (64 tokens of 8 requests, rank 128, 14.5 -> 17.7, in fp32 16.3 -> 19.6;
+// 32 of one, 12.5 -> 14.9; 8 of one, rank 64, 7.6 -> 7.5, rank 256 12.4 -> 18.6).
 constexpr int kXcds = 8, kNear = 2;
 __host__ __device__ inline bool near_halves(int halves, int ranks) { return ranks > 1 && halves >= kXcds * kNear; }
 __host__ __device__ inline long long lora_makers(long long halves, int each, bool near) {
@@ -615,7 +621,13 @@ __host__ __device__ inline long long lora_makers(long long halves, int each, boo
 }
 
 // The grid: `ranks` blocks of 32 ranks x a.splits parts of K of every half item,
-// then n_tiles tiles of columns of every half item.
+// then n_tiles tiles of columns of every half item.  Halves without tokens end at once,
+// but are dispatched, and the parts of K are fewer for them (2048 tokens of 8 requests, us:
+// rank 32, of 16 adapters 16.8, of 64 18.5, of 1024 23.3; rank 128 30.2, 30.6, 47.7).
+//
+// LDS: 48.5 / 54.5 / 66.5 / 90.5 KB for KS = 1 / 2 / 4 / 8, most of it v in three parts,
+// so that a CU of 160 KB has 3 / 2 / 2 / 1 workgroups; those that make v have the
+// same though they use 16 KB.  That is what bounds high ranks: at KS = 8 a SIMD has one wave.
 //
 // A workgroup of columns follows those that make its v in the grid, so alone on the
 // GPU it waits for what runs already.  Beside another such launch it may wait for
@@ -677,8 +689,8 @@ __global__ __launch_bounds__(kWaves* kWave, KS == 1 ? 3 : KS <= 4 ? 2 : 1) void 
 }
 
 // Up to four tokens, every workgroup with the whole of their v (4096 x 4096 at
-// rank 16, us: one token 4.5, of which a launch of any size is 2.7, with v handed over
-// 6.3).  No matrix instruction, whose operands would be turned round for the sake of
+// rank 16, us: one token 4.7, of which a launch that does nothing is 2.2, with v handed
+// over 6.4).  No matrix instruction, whose operands would be turned round for the sake of
 // 16 rows: loads as Sums', of which a lane takes the dot products with its 8 values of
 // each token, two values an instruction (off by at most 2^-22.5 of the magnitudes,
 // measured).  The lanes of a quad are added by lane exchanges, what else a row has in
@@ -871,12 +883,17 @@ hipError_t launch(const LoraArgs& a, hipStream_t st) {
 
 }  // namespace
 
-// Few tokens: see few_body (us: four tokens of one adapter at rank 16 6.6, else
-// 6.9; one at rank 32 6.2, 6.3; four 9.2, 6.7; one at rank 64 11.0, 7.7).  Else parts
-// of K until the workgroups that make v are about one and a half a CU (us, and with twice
-// as many, 4096 x 4096: 512 tokens of 64 adapters at rank 64 20.4, 20.0; 2048 of 8 requests
-// at rank 32 16.8, 17.0, at 64 22.0, 24.3, at 128 33.6, 35.4), with a step or more for
-// each wave.
+// Few tokens: see few_body (us, and with v handed over, 4096 x 4096: rank 16, one token
+// 4.7, 6.4; four 4.9, 6.8, of one adapter 6.7, 7.0; rank 32, one 6.2, 6.4; two 6.3, 6.9, of
+// one adapter 6.8, 6.6; four 6.7, 7.0, of one adapter 9.1, 7.1; one at rank 64 11.3, 7.2).
+// The time of v in each workgroup grows with K, which the rule leaves out: one token
+// at K = 1024 4.4, 5.7, at 14336 8.1, 7.5, at 28672 11.5, 8.7; at rank 32 5.1, 5.8, 11.2, 8.1
+// and 23, 10.
+// Else parts of K until the workgroups that make v are about one and a half a CU (us, and
+// with twice as many, 4096 x 4096: 512 tokens of 64 adapters, rank 64, 2048 columns, 16.1,
+// 16.9; 2048 of 8 requests at rank 32 16.8, 16.4, at 64 21.1, 22.9, at 128 30.9, 33.2), with a
+// step or more for each wave.  The guess of the runs is of adapters that are mostly in use:
+// of 1024 of which 8 are, rank 32 gets one part of K in place of four.
 LoraShape lora_shape(int T, int K, int N, int r, int L) {
     LoraShape p{0, 0, 0};
     if (r <= 32 && T * ceil_div(r, 16) <= 4) return p;

@@ -2,8 +2,8 @@
 // maximum m, S = sum e^(l - m), U = sum e^(l - m) (l - m) and the largest `top`
 // logits in one pass; then log p = l - m - ln S, the entropy ln S - U / S.
 //
-// Bound by HBM with many rows (each logit is read once; 2048 x 128256 bf16, top 5, 104
-// us, 5.1 TB/s), by latency with few: a row is then cut into parts (1 x 128256 8.5
+// Bound by HBM with many rows (each logit is read once; 2048 x 128256 bf16, top 5, 102
+// us, 5.1 TB/s of the 5.87 that reading alone reaches), by latency with few: a row is then cut into parts (1 x 128256 8.5
 // us, 77 x 50001 with top 20 13, 5 x 128256 fp32 without lists 5.6).
 //
 // A wave takes 16 bytes a lane and chunk, four chunks a round, the next round's on
