@@ -707,10 +707,11 @@ def _moe_type(dtype, name: str) -> int:
     raise ValueError(f"{name} has dtype {dtype}, expected torch.bfloat16 or torch.float32")
 
 
-def _sizes(where: str, *n: int) -> None:
-    """The C entry points take sizes of 32 bits, and ctypes cuts off what is
-    longer: a size that does not fit is refused here."""
-    if max(n) > 0x7fffffff or min(n) < -0x80000000:
+def _sizes(where: str, bits: int) -> None:
+    """`bits`: a call's sizes, or-ed.  The C entry points take them in 32 bits, and
+    ctypes cuts off what is longer: a size that is negative or does not fit is
+    refused here."""
+    if bits >> 31:
         raise MoeError(MOE_ERR_SHAPE, where)
 
 
@@ -1019,7 +1020,7 @@ class LoraPlan:
         dev = perm.get_device()
         if dev < 0:
             raise ValueError("LoraPlan takes device tensors")
-        _sizes("LoraPlan", T, adapters)
+        _sizes("LoraPlan", T | adapters)
         self.T, self.adapters, self.dev = T, adapters, dev
         self.perm, self.offsets, self.items = perm, offsets, items
         self.perm_addr = _addr(perm, i32, (T,), dev, "perm")
@@ -1037,7 +1038,7 @@ def lora_plan(ids, adapters: int, *, stream=None) -> LoraPlan:
             return lora_plan(ids, adapters)
     torch = _torch()
     T = ids.numel()
-    _sizes("moe_lora_plan", T, adapters)
+    _sizes("moe_lora_plan", T | adapters)
     idp = _addr(ids, (torch.int32,), (T,), dev, "ids")
     L = lib()
     n = L.moe_lora_items(T, adapters)
@@ -1076,7 +1077,7 @@ def lora_add(base, x, a, b, plan: LoraPlan, *, scales=None, out=None, ws=None, s
     bf16 = (torch.bfloat16,)
     T, N = shape = base.shape
     L, r, K = a.shape
-    _sizes("moe_lora_add", T, K, N, r, L)
+    _sizes("moe_lora_add", T | K | N | r | L)
     if x.dtype != torch.bfloat16 or x.shape != (T, K):
         raise ValueError(f"x must be torch.bfloat16 of shape {(T, K)}")
     if plan.T != T or plan.adapters != L:
@@ -1127,7 +1128,7 @@ def token_logprobs(logits, tokens=None, *, top: int = 0, entropy: bool = False, 
     f32, i32 = torch.float32, torch.int32
     lp, stride = _rows(logits, dev, "logits")
     T, V = logits.shape
-    _sizes("moe_token_logprobs", T, V, top)
+    _sizes("moe_token_logprobs", T | V | top)
     lt = _moe_type(logits.dtype, "logits")
     out = ent = ids = top_lp = None
     tp = outp = entp = idp = tlp = None
