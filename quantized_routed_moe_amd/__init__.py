@@ -760,6 +760,7 @@ def add_rmsnorm(x, weight=None, *, residual=None, residual_out=None, eps: float 
     xt = _moe_type(x.dtype, "x")
     shape = x.shape
     T, d = shape
+    _sizes("moe_add_rmsnorm", T | d)
     rp = rop = wp = yt = q = sc = yp = qp = sp = None
     rt = rs = ros = wt = 0
     bf16, f32 = torch.bfloat16, torch.float32
@@ -811,6 +812,7 @@ def gemm_fp8(a, a_scales, w, w_scales, *, out=None, out_dtype=None, stream=None)
     ap, lda = _rows(a, dev, "a")
     M, K = a.shape
     N = w.shape[0]
+    _sizes("moe_gemm_fp8", M | N | K)
     S = _runs(K)
     asp = _addr(a_scales, f32, (M, S), dev, "a_scales")
     wp = _addr(w, code, (N, K), dev, "w")
@@ -843,6 +845,7 @@ def grouped_gemm_fp8(a, a_scales, w, w_scales, offsets, *, perm=None, k: int = 1
     f32, i32, code = (torch.float32,), (torch.int32,), (torch.float8_e4m3fn, torch.uint8)
     a_rows, K = a.shape
     E, N, _ = w.shape
+    _sizes("moe_grouped_gemm_fp8", a_rows | K | E | N | k)
     S = _runs(K)
     ap = _addr(a, code, (a_rows, K), dev, "a")
     asp = _addr(a_scales, f32, (a_rows, S), dev, "a_scales")
@@ -852,6 +855,7 @@ def grouped_gemm_fp8(a, a_scales, w, w_scales, offsets, *, perm=None, k: int = 1
     R, permp = a_rows, None
     if perm is not None:
         R = perm.numel()
+        _sizes("moe_grouped_gemm_fp8", R)
         permp = _addr(perm, i32, (R,), dev, "perm")
     if out is None:
         out = a.new_empty((R, N), dtype=out_dtype or torch.float32)
@@ -884,6 +888,7 @@ def expert_gate_up_fp8(a, a_scales, gate, gate_scales, up, up_scales, offsets, p
     f32, i32, code = (torch.float32,), (torch.int32,), (torch.float8_e4m3fn, torch.uint8)
     T, d = a.shape
     E, f, _ = gate.shape
+    _sizes("moe_expert_gate_up_fp8", T | d | E | k | f)
     R, S, NB = T * k, _runs(d), _runs(f)
     ap = _addr(a, code, (T, d), dev, "a")
     asp = _addr(a_scales, f32, (T, S), dev, "a_scales")
@@ -983,6 +988,7 @@ def layer_fp8(x, xq, xq_scales, experts: ExpertsFp8, k: int, *, w_router=None, b
     T, d = xq.shape
     E = experts.E
     shape = Shape(T, d, E, k, experts.f)
+    _sizes("moe_layer_fp8", T | d | E | k | shape.f)
     xp = None if x is None else _addr(x, (torch.bfloat16,), (T, d), dev, "x")
     xqp = _addr(xq, (torch.float8_e4m3fn, torch.uint8), (T, d), dev, "xq")
     xsp = _addr(xq_scales, f32, (T, _runs(d)), dev, "xq_scales")
